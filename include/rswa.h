@@ -91,7 +91,9 @@ RSWA_API const char* rswa_last_error(void);
  * the page2d rotary encoding (rswa_rope_page2d, rswa_append_rope); 4 the FP8 ring
  * (rswa_append_fp8, rswa_decode_fp8kv, srswa_decode_fp8kv), the fused router
  * (srswa_decode_routed, srswa_step) and the wait-timeout test hook; 5 the fused steps
- * with the page2d encoding (rswa_decode_append_rope, srswa_step_rope). */
+ * with the page2d encoding (rswa_decode_append_rope, srswa_step_rope). rswa_rope_1d,
+ * rswa_decode_shared, rswa_decode_scored and rswa_prefill_scored came after it without a new
+ * number: they change nothing that a caller of version 5 uses. */
 RSWA_API int32_t rswa_version(void);
 
 /*
@@ -542,6 +544,48 @@ RSWA_API rswa_status srswa_step_rope(const rswa_dims* dims, const rswa_rope* rop
                                      void* ring_k, void* ring_v, int32_t* wp, int32_t* fill, int32_t* slot_out,
                                      float scale, int32_t* blk_idx, float* blk_logp, float* tau, float* out,
                                      float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Rotary encoding with one position per token, for decoders without a page axis (the v1
+ * model's LLaMA-family attention): pair i of the first rot_dim dims of a head turns by
+ * angle pos * inv_freq[i],
+ *   x' = mscale (x cos - y sin),  y' = mscale (y cos + x sin),
+ * dims from rot_dim on pass through. inverse = 1 applies the transpose (sin -> -sin): the
+ * gradient with respect to the input, given the gradient with respect to the output.
+ * Long-context scalings are tables of inv_freq (and mscale): any table is taken.
+ *   desc     : host pointer, read during the call only:
+ *     batch, heads_q, heads_k, tokens : rows are [batch][heads][tokens][head_dim]; heads_q
+ *                1..128, heads_k 0..128 (0: no k), batch and tokens >= 0 (0: nothing launched)
+ *     head_dim : a multiple of 16 in [16, 256];  rot_dim : a multiple of 16 in [16, head_dim]
+ *     layout   : RSWA_ROPE_HALF pairs dims (i, i + rot_dim / 2), RSWA_ROPE_INTERLEAVED (2i, 2i + 1)
+ *     dtype    : RSWA_DTYPE_BF16 or RSWA_DTYPE_F32, of every tensor
+ *     mscale   : finite factor on cos and sin (1 unless the scaling has one)
+ *     *_stride : strides of the batch, head and token axes in elements, each a multiple of 16
+ *                bytes (any order of the axes; the last axis is dense). Output rows must not
+ *                overlap one another.
+ *   inv_freq : HOST array f64 [rot_dim / 2], finite, read during the call only
+ *   pos      : int32 [batch][tokens], any values
+ *   q_out / k_out may be q / k with the same strides (in place; dims from rot_dim on are then
+ *   not touched); other overlaps of an output with an input are not supported.
+ * Arithmetic: the angle as a 64-bit fixed-point fraction of a turn (error below 2^-31 turns
+ * for every int32 position), cos / sin and the rotation in f32, one rounding to bf16: within
+ * 2^-20 (|x| + |y|) |mscale| plus half a bf16 step of the exact rotation by the table's angles.
+ */
+#define RSWA_ROPE_HALF 0
+#define RSWA_ROPE_INTERLEAVED 1
+#define RSWA_DTYPE_BF16 0
+#define RSWA_DTYPE_F32 1
+
+typedef struct rswa_rope1d {
+  int32_t batch, heads_q, heads_k, tokens;
+  int32_t head_dim, rot_dim;
+  int32_t layout, dtype, inverse;
+  float mscale;
+  int64_t q_stride[3], q_out_stride[3], k_stride[3], k_out_stride[3];
+} rswa_rope1d;
+
+RSWA_API rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_freq, const int32_t* pos, const void* q,
+                                  void* q_out, const void* k, void* k_out, void* stream);
 
 #ifdef __cplusplus
 }

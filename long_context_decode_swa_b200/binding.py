@@ -40,7 +40,7 @@ EXPORTED = ("rswa_last_error", "rswa_version", "rswa_workspace_bytes", "rswa_che
             "rswa_quantize_prefix", "rswa_decode_fp8", "srswa_decode_fp8", "srswa_route_tokens", "srswa_prefill",
             "rswa_decode_append", "srswa_decode_append", "rswa_rope_page2d", "rswa_append_rope", "rswa_append_fp8",
             "rswa_decode_fp8kv", "srswa_decode_fp8kv", "rswa_test_arm_wait_timeout", "srswa_decode_routed",
-            "srswa_step", "srswa_prefill_workspace_bytes", "rswa_decode_append_rope", "srswa_step_rope")
+            "srswa_step", "srswa_prefill_workspace_bytes", "rswa_decode_append_rope", "srswa_step_rope", "rswa_rope_1d")
 
 
 class RswaError(RuntimeError):
@@ -62,6 +62,14 @@ class Rope(ctypes.Structure):
     """rswa_rope: the page2d encoding of a fused decode step (device position arrays)."""
     _fields_ = [("tok_pos", ctypes.c_void_p), ("page", ctypes.c_void_p), ("base", ctypes.c_double),
                 ("page_mod", ctypes.c_int32)]
+
+
+class Rope1d(ctypes.Structure):
+    """rswa_rope1d: shapes and strides of a one-position rotary encoding."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "heads_q", "heads_k", "tokens", "head_dim", "rot_dim", "layout",
+                                              "dtype", "inverse")] + \
+        [("mscale", ctypes.c_float)] + \
+        [(n, ctypes.c_int64 * 3) for n in ("q_stride", "q_out_stride", "k_stride", "k_out_stride")]
 
 
 _lock = threading.Lock()
@@ -125,6 +133,7 @@ def load(path: str | None = None):
             "srswa_decode_fp8kv": ([DP, P, P, P, P, P, P, P, P, I32, P, P, P, P, P, P, F32, P, P, P, SZ, P],
                                    ctypes.c_int),
         }
+        sig["rswa_rope_1d"] = ([ctypes.POINTER(Rope1d), P, P, P, P, P, P, P], ctypes.c_int)
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
             f.argtypes = args
@@ -160,6 +169,44 @@ def _want(t: torch.Tensor, name: str, dtype, shape=None):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
+
+
+def _tensor(t, name: str, dtype, shape, device):
+    """A contiguous tensor of this dtype and shape on `device`: its address."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.device
+
+
+def _call(name: str, device, stream, *args):
+    """The C call on `stream` (default: the current stream of the tensors' device), with that device current."""
+    lib = load()
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == device.index:
+        code = getattr(lib, name)(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            code = getattr(lib, name)(*args, raw)
+    if code != 0:
+        _check(name, code)
 
 
 def dims_of(pk: torch.Tensor, ring_k: torch.Tensor) -> Dims:
@@ -239,6 +286,70 @@ def rswa_rope_page2d(q, tok_pos, page, q_out=None, k=None, k_out=None, base: flo
     _check("rswa_rope_page2d", load().rswa_rope_page2d(rows, H, D, _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out),
                                                        _ptr(tok_pos), _ptr(page), float(base), int(page_mod),
                                                        _stream(stream)))
+    return q_out, k_out
+
+
+def _rope_rows(t, name: str, dtype, lead, device):
+    """(address, (batch, head, token) strides) of rows [B][H][T][D] or [B][H][D] in any order of their axes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if lead is not None and t.shape != lead:
+        raise ValueError(f"{name}: expected shape {tuple(lead)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last axis must be dense")
+    return t.data_ptr(), (st[0], st[1], st[2] if len(st) == 4 else 0)
+
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str = "half", mscale: float = 1.0,
+                 inverse: bool = False, stream=None):
+    """Rotary encoding of q (and k), bf16 or f32 [B][H][T][D] at int32 positions pos [B][T], or [B][H][D]
+    with pos [B] (one token per sequence). q and k may differ in their number of heads, and every
+    tensor may be a strided view with a dense last axis. inv_freq: f64 pair frequencies on the host
+    (a CPU tensor; see rope_freqs); its length is half the rotated dims, the rest of a head passes
+    through. layout: "half" or "interleaved" pairs. inverse=True applies the transpose, which turns
+    gradients back. Outputs default to in place. Returns (q_out, k_out)."""
+    dev = _device_of(q, "q")
+    if q.dim() not in (3, 4):
+        raise ValueError("q: expected [B, H, T, D] or [B, H, D]")
+    if q.dtype not in _ROPE_DTYPES:
+        raise TypeError(f"q: expected torch.bfloat16 or torch.float32, got {q.dtype}")
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout: expected 'half' or 'interleaved', got {layout!r}")
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.is_cuda or inv_freq.dtype is not torch.float64 or \
+            inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq: expected a contiguous 1-D float64 tensor on the CPU")
+    B, T = q.shape[0], (q.shape[2] if q.dim() == 4 else 1)
+    d = Rope1d(B, q.shape[1], 0, T, q.shape[-1], 2 * inv_freq.shape[0], _ROPE_LAYOUTS[layout], _ROPE_DTYPES[q.dtype],
+               1 if inverse else 0, mscale)
+    qp, d.q_stride[:] = _rope_rows(q, "q", q.dtype, None, dev)
+    q_out = q if q_out is None else q_out
+    qop, d.q_out_stride[:] = _rope_rows(q_out, "q_out", q.dtype, q.shape, dev)
+    kp = kop = None
+    if k is not None:
+        shape = (B, k.shape[1]) + tuple(q.shape[2:]) if isinstance(k, torch.Tensor) and k.dim() == q.dim() else q.shape
+        kp, d.k_stride[:] = _rope_rows(k, "k", q.dtype, shape, dev)
+        k_out = k if k_out is None else k_out
+        kop, d.k_out_stride[:] = _rope_rows(k_out, "k_out", q.dtype, k.shape, dev)
+        d.heads_k = k.shape[1]
+        if d.heads_k == 0:
+            raise ValueError("k: has no heads (pass None)")
+    elif k_out is not None:
+        raise ValueError("k_out given without k")
+    for src, dst, si, so, name in ((qp, qop, d.q_stride, d.q_out_stride, "q_out"),
+                                   (kp, kop, d.k_stride, d.k_out_stride, "k_out")):
+        if src is not None and src == dst and si[:] != so[:]:
+            raise ValueError(f"{name}: in place needs the input's strides")
+    _call("rswa_rope_1d", dev, stream, d, inv_freq.data_ptr(),
+          _tensor(pos, "pos", torch.int32, (B, T) if q.dim() == 4 else (B,), dev), qp, qop, kp, kop)
     return q_out, k_out
 
 

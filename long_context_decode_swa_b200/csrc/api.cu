@@ -3,6 +3,7 @@
 // Every entry point validates its arguments on the host before launching
 // anything, records a message for rswa_last_error() on failure, and only
 // enqueues work on the caller's stream.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1017,6 +1018,79 @@ rswa_status rswa_decode_noalloc(const rswa_dims* dims, const void* q, const void
     e = cudaMemcpyAsync(status, scratch, sizeof(int32_t), cudaMemcpyDeviceToDevice, s);
     if (e != cudaSuccess) return cuda_fail(e, "rswa_decode_noalloc: copying the status word");
   }
+  return ok();
+}
+
+rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_freq, const int32_t* pos, const void* q,
+                         void* q_out, const void* k, void* k_out, void* stream) {
+  const char* fn = "rswa_rope_1d";
+  const NvtxRange nvtx_range(fn);
+  if (desc == nullptr) return fail(RSWA_ERR_INVALID, "%s: desc must not be NULL", fn);
+  const rswa_rope1d& d = *desc;
+  if (d.batch < 0 || d.tokens < 0)
+    return fail(RSWA_ERR_INVALID, "%s: batch and tokens must be >= 0 (got %d, %d)", fn, d.batch, d.tokens);
+  if (d.heads_q < 1 || d.heads_q > 128 || d.heads_k < 0 || d.heads_k > 128)
+    return fail(RSWA_ERR_INVALID, "%s: heads_q must be in [1, 128] and heads_k in [0, 128] (got %d, %d)", fn, d.heads_q,
+                d.heads_k);
+  if (d.head_dim < 16 || d.head_dim > 256 || d.head_dim % 16 != 0)
+    return fail(RSWA_ERR_UNSUPPORTED, "%s: head_dim must be a multiple of 16 in [16, 256] (got %d)", fn, d.head_dim);
+  if (d.rot_dim < 16 || d.rot_dim > d.head_dim || d.rot_dim % 16 != 0)
+    return fail(RSWA_ERR_UNSUPPORTED, "%s: rot_dim must be a multiple of 16 in [16, head_dim] (got %d)", fn, d.rot_dim);
+  if (d.layout != RSWA_ROPE_HALF && d.layout != RSWA_ROPE_INTERLEAVED)
+    return fail(RSWA_ERR_INVALID, "%s: unknown layout %d", fn, d.layout);
+  if (d.dtype != RSWA_DTYPE_BF16 && d.dtype != RSWA_DTYPE_F32)
+    return fail(RSWA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, d.dtype);
+  if (!std::isfinite(d.mscale)) return fail(RSWA_ERR_INVALID, "%s: mscale must be finite", fn);
+  if (inv_freq == nullptr) return fail(RSWA_ERR_INVALID, "%s: inv_freq must not be NULL", fn);
+  if (d.batch == 0 || d.tokens == 0) return ok();  // nothing to encode; the (empty) buffers may be NULL
+  REQUIRE_PTR(q);
+  REQUIRE_PTR(q_out);
+  if (pos == nullptr) return fail(RSWA_ERR_INVALID, "%s: pos must not be NULL", fn);
+  if (d.heads_k > 0) {
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(k_out);
+  }
+  const int64_t vec = d.dtype == RSWA_DTYPE_F32 ? 4 : 8;
+  const int64_t* all[4] = {d.q_stride, d.q_out_stride, d.k_stride, d.k_out_stride};
+  const char* names[4] = {"q", "q_out", "k", "k_out"};
+  for (int i = 0; i < (d.heads_k > 0 ? 4 : 2); ++i) {
+    const int32_t extent[3] = {d.batch, i < 2 ? d.heads_q : d.heads_k, d.tokens};
+    for (int j = 0; j < 3; ++j) {
+      if (all[i][j] % vec != 0)
+        return fail(RSWA_ERR_INVALID, "%s: strides of %s must be multiples of 16 bytes", fn, names[i]);
+      if ((i & 1) && extent[j] > 1 && all[i][j] == 0)
+        return fail(RSWA_ERR_INVALID, "%s: rows of %s overlap (a stride of 0)", fn, names[i]);
+    }
+  }
+  rswa::Rope1dLaunch L;
+  L.B = d.batch;
+  L.Hq = d.heads_q;
+  L.Hk = d.heads_k;
+  L.T = d.tokens;
+  L.D = d.head_dim;
+  L.rot = d.rot_dim;
+  L.interleaved = d.layout == RSWA_ROPE_INTERLEAVED;
+  L.f32 = d.dtype == RSWA_DTYPE_F32;
+  L.inverse = d.inverse != 0;
+  L.copy_rest = q != q_out || (d.heads_k > 0 && k != k_out);
+  L.mscale = d.mscale;
+  L.q = q;
+  L.q_out = q_out;
+  L.k = k;
+  L.k_out = k_out;
+  L.q_stride = d.q_stride;
+  L.q_out_stride = d.q_out_stride;
+  L.k_stride = d.k_stride;
+  L.k_out_stride = d.k_out_stride;
+  L.pos = pos;
+  for (int i = 0; i < d.rot_dim / 2; ++i) {
+    if (!std::isfinite(inv_freq[i])) return fail(RSWA_ERR_INVALID, "%s: inv_freq[%d] is not finite", fn, i);
+    // turns per position modulo 1 in 64-bit fixed point; whole turns do not matter to an integer position
+    const long double turns = (long double)inv_freq[i] * 0.159154943091895335768883763372514362L;  // 1 / (2 pi)
+    L.turns[i] = (uint64_t)((turns - floorl(turns)) * 18446744073709551616.0L);
+  }
+  cudaError_t e = rswa::launch_rope1d(L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
 }
 

@@ -126,6 +126,25 @@ cudaError_t launch_append_rope(int B, int H, int n, uint16_t* ring_k, uint16_t* 
                                const uint16_t* v_new, const uint16_t* q, uint16_t* q_out, const int32_t* tok_pos,
                                const int32_t* page, double base, int page_mod, int32_t* wp, int32_t* fill,
                                int32_t* slot_out, int32_t* status, cudaStream_t stream);
+// One-position rotary encoding over strided rows [B][H][T][D] of q and k (strides: batch, head,
+// token, in elements; the last dim is dense). turns[i]: frac(inv_freq[i] / 2 pi) * 2^64.
+struct Rope1dLaunch {
+  int B, Hq, Hk, T, D, rot;
+  int interleaved, f32, inverse;
+  int copy_rest;  // some output is not its own input: dims from rot on are copied
+  float mscale;
+  const void* q;
+  void* q_out;
+  const void* k;
+  void* k_out;
+  const int64_t* q_stride;
+  const int64_t* q_out_stride;
+  const int64_t* k_stride;
+  const int64_t* k_out_stride;
+  const int32_t* pos;
+  uint64_t turns[128];
+};
+cudaError_t launch_rope1d(const Rope1dLaunch& L, cudaStream_t stream);
 cudaError_t launch_quantize_prefix(int B, int H, int64_t cap, const uint16_t* pk, const uint16_t* pv,
                                    const int32_t* prefix_len, uint8_t* pk8, uint8_t* pv8, float* k_scale,
                                    float* v_scale, int32_t* status, cudaStream_t stream);

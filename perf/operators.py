@@ -248,8 +248,8 @@ def _workspace(rswa, c):
     key = (c["op"], c["B"], c["H"], c["n"], c["cap"], c.get("P"), c.get("scap"))
     if key not in _workspaces:
         dims = rswa.Dims(c["B"], c["H"], D, c["n"], c["cap"])
-        _workspaces[key] = (rswa.new_shared_workspace(dims, c["P"], c["scap"]) if c["op"] == "shared" else
-                            rswa.new_workspace(dims, rswa.OP_DECODE if c["op"] == "decode" else rswa.OP_PREFILL))
+        _workspaces[key] = (rswa.new_shared_workspace(dims, c["P"]) if c["op"] == "shared" else
+                            rswa.new_workspace(dims, rswa.OP_DECODE_SCORED if c["op"] == "decode" else rswa.OP_PREFILL))
     return _workspaces[key]
 
 

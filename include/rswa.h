@@ -66,6 +66,9 @@ typedef enum {
 #define RSWA_DEVICE_BAD_BLOCK_IDX 0x4  /* blk_idx entry >= number of prefix blocks: entry skipped    */
 #define RSWA_DEVICE_WAIT_TIMEOUT 0x8   /* a bounded pipeline wait gave up (the output is not valid)  */
 #define RSWA_DEVICE_PIPELINE 0x10      /* a pipeline stage held an unexpected tile (output not valid) */
+#define RSWA_DEVICE_BAD_RANGE 0x20 /* a row range not within the prefix: the query sees no prefix row    */
+#define RSWA_DEVICE_BAD_POS 0x40   /* pos[b] < 0 or > 2^30: the sequence's prefix skipped              */
+#define RSWA_DEVICE_BAD_SHARE 0x80 /* share_of[b] < -1 or >= the number of prefixes: read as -1          */
 
 typedef struct {
   int32_t batch;      /* B: sequences                                                   */
@@ -82,6 +85,7 @@ typedef struct {
 #define RSWA_OP_ROUTE 3         /* srswa_route, srswa_route_tokens (256 bytes)               */
 #define RSWA_OP_PREFILL 4       /* rswa_prefill (256 bytes); srswa_prefill: srswa_prefill_workspace_bytes */
 #define RSWA_OP_SRSWA_ROUTED 5  /* srswa_decode_routed, srswa_step (any topk in 1..32)       */
+#define RSWA_OP_DECODE_SCORED 6 /* rswa_decode_scored                                        */
 
 /* Message of the last failed call on this host thread ("" if none). */
 RSWA_API const char* rswa_last_error(void);
@@ -586,6 +590,66 @@ typedef struct rswa_rope1d {
 
 RSWA_API rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_freq, const int32_t* pos, const void* q,
                                   void* q_out, const void* k, void* k_out, void* stream);
+
+/*
+ * R-SWA decode with scores that are more than scale * q.k: for every (b, h), over the prefix
+ * rows [lo, hi) of the query's document and the ring's valid slots,
+ *   s = cap tanh(scale q.k / cap)  (softcap = cap > 0; 0: scale q.k)  - slope[h] (pos_q - pos_k),
+ *   out[b][h] = softmax(s) V.
+ * pos_q = pos[b] is the query's position on the line of all tokens (prefix, then every output),
+ * prefix row x is at position x, and the r-th most recently written ring slot at pos[b] - (r - 1)
+ * (the newest slot is the query's own token, as after rswa_append).
+ * Arguments as rswa_decode (workspace: RSWA_OP_DECODE_SCORED), and
+ *   score : host pointer, read during the call only
+ *     softcap : finite, >= 0
+ *     slope   : f32 [heads] device array of finite values, or NULL (no distance bias)
+ *     pos     : int32 [batch] device array, with slope: each in [0, 2^30] (others: flagged
+ *               RSWA_DEVICE_BAD_POS, the sequence's prefix is skipped); NULL without
+ *     range   : int32 [batch][2] device array (8-byte aligned): lo, hi; lo >= hi: no prefix row;
+ *               not within [0, prefix_len[b]]: flagged RSWA_DEVICE_BAD_RANGE, no prefix row; or
+ *               NULL: the whole prefix
+ * A query that sees no row at all has out 0 and lse -inf. Rows outside the range are not read.
+ * The distance bias is taken relative to the query's most favoured row, in integers, so far
+ * documents lose no precision. prefix_cap may be 0 (pk, pv, prefix_len are then not read).
+ */
+typedef struct rswa_score {
+  float softcap;
+  const float* slope;
+  const int32_t* pos;
+  const int32_t* range;
+} rswa_score;
+
+RSWA_API rswa_status rswa_decode_scored(const rswa_dims* dims, const rswa_score* score, const void* q, const void* pk,
+                                        const void* pv, const int32_t* prefix_len, const void* ring_k,
+                                        const void* ring_v, const int32_t* wp, const int32_t* fill, float scale,
+                                        float* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * R-SWA decode of sequences that share prefixes: sequence b attends to the rows
+ * [0, shared_len[p]) of shared prefix p = share_of[b] (none if -1), to its private prefix rows
+ * [0, prefix_len[b]) and to its ring's valid slots, in one softmax. Every shared row is read once
+ * for up to 256 sequences (three launches: grouping, the shared part on the tensor cores with the
+ * weights rounded to bf16, the private part in f32 joined with it).
+ *   dims       : as rswa_decode; prefix_cap is the PRIVATE capacity and may be 0 (pk, pv and
+ *                prefix_len are then not read and may be NULL)
+ *   n_shared   : prefixes P, 1..8192;  shared_cap : rows allocated for each, 1..2^30
+ *   sk, sv     : bf16 [P][H][shared_cap][D];  shared_len : int32 [P], each in [0, shared_cap]
+ *                (others: flagged RSWA_DEVICE_BAD_PREFIX_LEN, read as 0)
+ *   share_of   : int32 [B] in [-1, P) (others: flagged RSWA_DEVICE_BAD_SHARE, read as -1)
+ *   out        : bf16 [B][H][D] (the precision that bf16 weights carry);  lse : f32 [B][H] or NULL
+ *   workspace  : zero-initialised, rswa_decode_shared_workspace_bytes(dims, n_shared) bytes
+ *   A sequence that sees no row has out 0 and lse -inf. Rows at or past a length are not used,
+ *   whatever they hold; all other rows must be finite.
+ * Unsupported: n_shared * heads * shared_cap at or above 2^31 rows.
+ */
+RSWA_API size_t rswa_decode_shared_workspace_bytes(const rswa_dims* dims, int32_t n_shared);
+
+RSWA_API rswa_status rswa_decode_shared(const rswa_dims* dims, int32_t n_shared, int64_t shared_cap, const void* q,
+                                        const void* sk, const void* sv, const int32_t* shared_len,
+                                        const int32_t* share_of, const void* pk, const void* pv,
+                                        const int32_t* prefix_len, const void* ring_k, const void* ring_v,
+                                        const int32_t* wp, const int32_t* fill, float scale, void* out, float* lse,
+                                        void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

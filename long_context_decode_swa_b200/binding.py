@@ -26,6 +26,7 @@ OP_SRSWA_DECODE = 2
 OP_ROUTE = 3
 OP_PREFILL = 4
 OP_SRSWA_ROUTED = 5
+OP_DECODE_SCORED = 6
 
 STATUS_NAMES = {0: "RSWA_OK", 1: "RSWA_ERR_INVALID", 2: "RSWA_ERR_UNSUPPORTED", 3: "RSWA_ERR_CUDA",
                 5: "RSWA_ERR_DEVICE_CHECK"}
@@ -34,13 +35,17 @@ DEVICE_BAD_RING_STATE = 0x2
 DEVICE_BAD_BLOCK_IDX = 0x4
 DEVICE_WAIT_TIMEOUT = 0x8
 DEVICE_PIPELINE = 0x10
+DEVICE_BAD_RANGE = 0x20
+DEVICE_BAD_POS = 0x40
+DEVICE_BAD_SHARE = 0x80
 
 EXPORTED = ("rswa_last_error", "rswa_version", "rswa_workspace_bytes", "rswa_check_status", "rswa_append",
             "rswa_decode", "srswa_index_pool", "srswa_route", "srswa_decode", "rswa_decode_noalloc", "rswa_prefill",
             "rswa_quantize_prefix", "rswa_decode_fp8", "srswa_decode_fp8", "srswa_route_tokens", "srswa_prefill",
             "rswa_decode_append", "srswa_decode_append", "rswa_rope_page2d", "rswa_append_rope", "rswa_append_fp8",
             "rswa_decode_fp8kv", "srswa_decode_fp8kv", "rswa_test_arm_wait_timeout", "srswa_decode_routed",
-            "srswa_step", "srswa_prefill_workspace_bytes", "rswa_decode_append_rope", "srswa_step_rope", "rswa_rope_1d")
+            "srswa_step", "srswa_prefill_workspace_bytes", "rswa_decode_append_rope", "srswa_step_rope", "rswa_rope_1d",
+            "rswa_decode_scored", "rswa_decode_shared", "rswa_decode_shared_workspace_bytes")
 
 
 class RswaError(RuntimeError):
@@ -62,6 +67,12 @@ class Rope(ctypes.Structure):
     """rswa_rope: the page2d encoding of a fused decode step (device position arrays)."""
     _fields_ = [("tok_pos", ctypes.c_void_p), ("page", ctypes.c_void_p), ("base", ctypes.c_double),
                 ("page_mod", ctypes.c_int32)]
+
+
+class Score(ctypes.Structure):
+    """rswa_score: the cap, distance bias and document ranges of scored attention (device arrays)."""
+    _fields_ = [("softcap", ctypes.c_float), ("slope", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("range", ctypes.c_void_p)]
 
 
 class Rope1d(ctypes.Structure):
@@ -134,6 +145,11 @@ def load(path: str | None = None):
                                    ctypes.c_int),
         }
         sig["rswa_rope_1d"] = ([ctypes.POINTER(Rope1d), P, P, P, P, P, P, P], ctypes.c_int)
+        sig["rswa_decode_scored"] = ([DP, ctypes.POINTER(Score), P, P, P, P, P, P, P, P, F32, P, P, P, SZ, P],
+                                     ctypes.c_int)
+        sig["rswa_decode_shared_workspace_bytes"] = ([DP, I32], SZ)
+        sig["rswa_decode_shared"] = ([DP, I32, I64, P, P, P, P, P, P, P, P, P, P, P, P, F32, P, P, P, SZ, P],
+                                     ctypes.c_int)
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
             f.argtypes = args
@@ -916,3 +932,104 @@ def srswa_step_rope(q, k_new, v_new, q_idx, kbar, pk, pv, prefix_len, ring_k, ri
         float(idx_scale), topk, _ptr(pk), _ptr(pv), _ptr(prefix_len), _ptr(ring_k), _ptr(ring_v), _ptr(wp),
         _ptr(fill), _ptr(slot_out), scale, _ptr(blk_idx), _ptr(blk_logp), _ptr(tau), _ptr(out), _ptr(lse),
         _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def _workspace(t, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
+    if t.dtype is not torch.uint8:
+        raise TypeError(f"workspace: expected torch.uint8, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"workspace: expected a tensor on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return t.data_ptr(), t.numel()
+
+
+def _score(softcap, slopes, pos, ranges, heads: int, lead, device):
+    """rswa_score of queries [*lead]: slopes [heads] with pos [B], ranges [*lead, 2]."""
+    if slopes is not None and pos is None:
+        raise ValueError("slopes need pos")
+    s = Score(softcap, None, None, None)
+    if slopes is not None:
+        s.slope = _tensor(slopes, "slopes", torch.float32, (heads,), device)
+        s.pos = _tensor(pos, "pos", torch.int32, lead[:1], device)
+    if ranges is not None:
+        s.range = _tensor(ranges, "ranges", torch.int32, (*lead, 2), device)
+    return s
+
+
+def _ring(ring_k, ring_v, wp, fill, B: int, H: int, D: int, device):
+    if not isinstance(ring_k, torch.Tensor) or ring_k.dim() != 4:
+        raise ValueError("ring_k: expected a tensor [B, H, n, D]")
+    shape = (B, H, ring_k.shape[2], D)
+    return (_tensor(ring_k, "ring_k", torch.bfloat16, shape, device),
+            _tensor(ring_v, "ring_v", torch.bfloat16, shape, device),
+            _tensor(wp, "wp", torch.int32, (B,), device), _tensor(fill, "fill", torch.int32, (B,), device))
+
+
+def rswa_decode_scored(q, pk, pv, prefix_len, ring_k, ring_v, wp, fill, out, workspace, softcap: float = 0.0,
+                       slopes=None, pos=None, ranges=None, lse=None, scale=None, stream=None):
+    """R-SWA decode whose scores are softcap * tanh(scale q.k / softcap) (softcap > 0) minus
+    slopes[h] * (pos - key position), over prefix rows ranges[b] = (lo, hi) and the ring. q bf16
+    [B][H][D]; slopes f32 [H] with pos int32 [B]; ranges int32 [B][2]; out f32 [B][H][D], lse f32
+    [B][H]. workspace: new_workspace(dims, OP_DECODE_SCORED)."""
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or not isinstance(pk, torch.Tensor) or pk.dim() != 4:
+        raise ValueError("expected q [B, H, D] and pk [B, H, cap, D]")
+    B, H, D = q.shape
+    cap = pk.shape[2]
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    rk, rv, w, f = _ring(ring_k, ring_v, wp, fill, B, H, D, dev)
+    score = _score(softcap, slopes, pos, ranges, H, (B,), dev)
+    wsp, wsn = _workspace(workspace, dev)
+    _call("rswa_decode_scored", dev, stream, Dims(B, H, D, ring_k.shape[2], cap), score, _tensor(q, "q", bf16, (B, H, D), dev),
+          _tensor(pk, "pk", bf16, (B, H, cap, D), dev), _tensor(pv, "pv", bf16, (B, H, cap, D), dev),
+          _tensor(prefix_len, "prefix_len", i32, (B,), dev), rk, rv, w, f,
+          1.0 / math.sqrt(D) if scale is None else scale, _tensor(out, "out", f32, (B, H, D), dev),
+          None if lse is None else _tensor(lse, "lse", f32, (B, H), dev), wsp, wsn)
+
+
+def shared_workspace_bytes(dims: Dims, n_shared: int) -> int:
+    """Workspace bytes of rswa_decode_shared; dims.prefix_cap is the private capacity."""
+    n = load().rswa_decode_shared_workspace_bytes(ctypes.byref(dims), n_shared)
+    if n == 0:
+        raise RswaError("rswa_decode_shared_workspace_bytes", 1, load().rswa_last_error().decode())
+    return int(n)
+
+
+def new_shared_workspace(dims: Dims, n_shared: int, device=None) -> torch.Tensor:
+    """A zero-filled workspace tensor (uint8) for rswa_decode_shared over n_shared prefixes."""
+    return torch.zeros(shared_workspace_bytes(dims, n_shared), dtype=torch.uint8, device=device or "cuda")
+
+
+def rswa_decode_shared(q, sk, sv, shared_len, share_of, ring_k, ring_v, wp, fill, out, workspace, pk=None, pv=None,
+                       prefix_len=None, lse=None, scale=None, stream=None):
+    """R-SWA decode of sequences over shared prefixes sk / sv bf16 [P][H][cap][D] (shared_len int32 [P]):
+    sequence b reads prefix share_of[b] (int32 [B], -1: none), its private prefix (pk, pv, prefix_len as
+    in rswa_decode; optional) and its ring. q bf16 [B][H][D]; out bf16 [B][H][D], lse f32 [B][H].
+    workspace: new_shared_workspace(Dims(B, H, D, n, private cap), P)."""
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or not isinstance(sk, torch.Tensor) or sk.dim() != 4:
+        raise ValueError("expected q [B, H, D] and sk [P, H, cap, D]")
+    B, H, D = q.shape
+    P, _, scap, _ = sk.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    cap, kp, vp, np_ = 0, None, None, None
+    if pk is not None:
+        if not isinstance(pk, torch.Tensor) or pk.dim() != 4:
+            raise ValueError("pk: expected a tensor [B, H, cap, D]")
+        cap = pk.shape[2]
+        kp = _tensor(pk, "pk", bf16, (B, H, cap, D), dev)
+        vp = _tensor(pv, "pv", bf16, (B, H, cap, D), dev)
+        np_ = _tensor(prefix_len, "prefix_len", i32, (B,), dev)
+    elif pv is not None or prefix_len is not None:
+        raise ValueError("pk, pv and prefix_len go together")
+    rk, rv, w, f = _ring(ring_k, ring_v, wp, fill, B, H, D, dev)
+    wsp, wsn = _workspace(workspace, dev)
+    _call("rswa_decode_shared", dev, stream, Dims(B, H, D, ring_k.shape[2], cap), P, scap,
+          _tensor(q, "q", bf16, (B, H, D), dev), _tensor(sk, "sk", bf16, (P, H, scap, D), dev),
+          _tensor(sv, "sv", bf16, (P, H, scap, D), dev), _tensor(shared_len, "shared_len", i32, (P,), dev),
+          _tensor(share_of, "share_of", i32, (B,), dev), kp, vp, np_, rk, rv, w, f,
+          1.0 / math.sqrt(D) if scale is None else scale, _tensor(out, "out", bf16, (B, H, D), dev),
+          None if lse is None else _tensor(lse, "lse", torch.float32, (B, H), dev), wsp, wsn)

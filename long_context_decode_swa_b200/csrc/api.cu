@@ -11,8 +11,10 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "balanced.h"
 #include "common.cuh"
 #include "internal.h"
+#include "shared.h"
 
 namespace {
 
@@ -110,6 +112,8 @@ size_t rswa_workspace_bytes(const rswa_dims* dims, int32_t op) {
       }
       return most;
     }
+    case RSWA_OP_DECODE_SCORED:
+      return 256 + rswa::balanced_scratch_bytes();
     case RSWA_OP_SRSWA_DECODE: {
       // the plan depends on topk (and the fused append's extra tile): size for the largest
       size_t most = 0;
@@ -1090,6 +1094,135 @@ rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_freq, const 
     L.turns[i] = (uint64_t)((turns - floorl(turns)) * 18446744073709551616.0L);
   }
   cudaError_t e = rswa::launch_rope1d(L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+// What the evenly cut decode calls have in common: their checks, and the arguments of the launch.
+static rswa_status balanced_args(const char* fn, const rswa_dims* dims, const void* q, const void* pk, const void* pv,
+                                 const int32_t* prefix_len, const void* ring_k, const void* ring_v, const int32_t* wp,
+                                 const int32_t* fill, float scale, void* out, float* lse, void* workspace,
+                                 rswa::BalancedArgs* a) {
+  rswa_status st = check_dims(fn, dims, true);
+  if (st != RSWA_OK) return st;
+  REQUIRE_PTR(q);
+  if (dims->prefix_cap > 0) {
+    REQUIRE_PTR(pk);
+    REQUIRE_PTR(pv);
+    if (prefix_len == nullptr) return fail(RSWA_ERR_INVALID, "%s: prefix_len must not be NULL", fn);
+  }
+  REQUIRE_PTR(ring_k);
+  REQUIRE_PTR(ring_v);
+  if (wp == nullptr || fill == nullptr) return fail(RSWA_ERR_INVALID, "%s: wp and fill must not be NULL", fn);
+  REQUIRE_PTR(out);
+  REQUIRE_PTR(workspace);
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RSWA_ERR_INVALID, "%s: scale must be finite and > 0", fn);
+  *a = rswa::BalancedArgs{};
+  a->B = dims->batch;
+  a->H = dims->heads;
+  a->n = dims->ring;
+  a->cap = dims->prefix_cap;
+  a->q = static_cast<const uint16_t*>(q);
+  a->pk = static_cast<const uint16_t*>(pk);
+  a->pv = static_cast<const uint16_t*>(pv);
+  a->prefix_len = prefix_len;
+  a->ring_k = static_cast<const uint16_t*>(ring_k);
+  a->ring_v = static_cast<const uint16_t*>(ring_v);
+  a->wp = wp;
+  a->fill = fill;
+  a->scale = scale;
+  a->out = out;
+  a->lse = lse;
+  a->status = ws_status(workspace);
+  return RSWA_OK;
+}
+
+// A score's own checks.
+static rswa_status check_score(const char* fn, const rswa_score* s) {
+  if (s == nullptr) return fail(RSWA_ERR_INVALID, "%s: score must not be NULL", fn);
+  if (!(s->softcap >= 0.f) || !std::isfinite(s->softcap))
+    return fail(RSWA_ERR_INVALID, "%s: softcap must be finite and >= 0", fn);
+  if ((s->slope == nullptr) != (s->pos == nullptr))
+    return fail(RSWA_ERR_INVALID, "%s: slope and pos must both be given or both be NULL", fn);
+  if (s->range != nullptr && (reinterpret_cast<uintptr_t>(s->range) & 7u) != 0)
+    return fail(RSWA_ERR_INVALID, "%s: range is not 8-byte aligned", fn);
+  return RSWA_OK;
+}
+
+rswa_status rswa_decode_scored(const rswa_dims* dims, const rswa_score* score, const void* q, const void* pk,
+                               const void* pv, const int32_t* prefix_len, const void* ring_k, const void* ring_v,
+                               const int32_t* wp, const int32_t* fill, float scale, float* out, float* lse,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "rswa_decode_scored";
+  const NvtxRange nvtx_range(fn);
+  rswa::BalancedArgs a;
+  rswa_status st =
+      balanced_args(fn, dims, q, pk, pv, prefix_len, ring_k, ring_v, wp, fill, scale, out, lse, workspace, &a);
+  if (st != RSWA_OK) return st;
+  if ((st = check_score(fn, score)) != RSWA_OK) return st;
+  const size_t need = 256 + rswa::balanced_scratch_bytes();
+  if (ws_bytes < need)
+    return fail(RSWA_ERR_INVALID, "%s: workspace of %zu bytes is smaller than the %zu required", fn, ws_bytes, need);
+  a.softcap = score->softcap;
+  a.slopes = score->slope;
+  a.pos = score->pos;
+  a.ranges = reinterpret_cast<const int2*>(score->range);
+  cudaError_t e =
+      rswa::launch_balanced(a, static_cast<uint8_t*>(workspace) + 256, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+size_t rswa_decode_shared_workspace_bytes(const rswa_dims* dims, int32_t n_shared) {
+  const char* fn = "rswa_decode_shared_workspace_bytes";
+  if (check_dims(fn, dims, true) != RSWA_OK) return 0;
+  if (n_shared < 1 || n_shared > rswa::kMaxShared) {
+    fail(RSWA_ERR_INVALID, "%s: n_shared must be in [1, %d] (got %d)", fn, rswa::kMaxShared, n_shared);
+    return 0;
+  }
+  return 256 + align256(rswa::balanced_scratch_bytes()) + rswa::plan_shared(dims->batch, dims->heads, n_shared).bytes;
+}
+
+rswa_status rswa_decode_shared(const rswa_dims* dims, int32_t n_shared, int64_t shared_cap, const void* q,
+                               const void* sk, const void* sv, const int32_t* shared_len, const int32_t* share_of,
+                               const void* pk, const void* pv, const int32_t* prefix_len, const void* ring_k,
+                               const void* ring_v, const int32_t* wp, const int32_t* fill, float scale, void* out,
+                               float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "rswa_decode_shared";
+  const NvtxRange nvtx_range(fn);
+  rswa::BalancedArgs a;
+  rswa_status st =
+      balanced_args(fn, dims, q, pk, pv, prefix_len, ring_k, ring_v, wp, fill, scale, out, lse, workspace, &a);
+  if (st != RSWA_OK) return st;
+  REQUIRE_PTR(sk);
+  REQUIRE_PTR(sv);
+  if (shared_len == nullptr || share_of == nullptr)
+    return fail(RSWA_ERR_INVALID, "%s: shared_len and share_of must not be NULL", fn);
+  if (n_shared < 1 || n_shared > rswa::kMaxShared)
+    return fail(RSWA_ERR_INVALID, "%s: n_shared must be in [1, %d] (got %d)", fn, rswa::kMaxShared, n_shared);
+  if (shared_cap < 1 || shared_cap > (int64_t)1 << 30)
+    return fail(RSWA_ERR_INVALID, "%s: shared_cap out of range (got %lld)", fn, (long long)shared_cap);
+  if ((int64_t)n_shared * dims->heads * shared_cap >= ((int64_t)1 << 31) - 1)
+    return fail(RSWA_ERR_UNSUPPORTED, "%s: more than 2^31 shared rows", fn);
+  const size_t need = rswa_decode_shared_workspace_bytes(dims, n_shared);
+  if (ws_bytes < need)
+    return fail(RSWA_ERR_INVALID, "%s: workspace of %zu bytes is smaller than the %zu required", fn, ws_bytes, need);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  rswa::SharedLaunch L;
+  L.B = dims->batch;
+  L.H = dims->heads;
+  L.P = n_shared;
+  L.cap = shared_cap;
+  L.q = static_cast<const uint16_t*>(q);
+  L.sk = sk;
+  L.sv = sv;
+  L.shared_len = shared_len;
+  L.share_of = share_of;
+  L.scale = scale;
+  L.status = a.status;
+  cudaError_t e = rswa::launch_shared(L, ws + 256 + align256(rswa::balanced_scratch_bytes()), &a.shared,
+                                      static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = rswa::launch_balanced(a, ws + 256, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
 }

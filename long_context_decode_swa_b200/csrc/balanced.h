@@ -1,0 +1,74 @@
+// balanced.h -- the evenly cut single-token attention (balanced.cu) and the tables and records
+// that the shared part of shared-prefix decode (shared.cu) hands to it.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace rswa {
+
+constexpr int kMaxPos = 1 << 30;       // largest query position of a distance bias
+constexpr int kRecordFloats = 4 + 128;  // max, sum of the weights that met V, sum of the weights, -, accumulator
+constexpr int kSharedRows = 256;        // sequences that one pass over a shared prefix serves
+
+// Up to kSharedRows sequences over one shared prefix. Units of the shared part: key tiles of 128,
+// a tile's heads one after the other.
+struct SharedTile {
+  long long first_unit;
+  int first_seq;  // its sequences: order[first_seq .. first_seq + rows)
+  int rows;
+  int prefix;
+  int len;        // rows of the prefix
+  int key_tiles;
+  int pad;
+};
+
+struct SharedHead {
+  long long units;  // of all tiles and heads
+  long long per;    // units a CTA takes: CTA c has [c per, (c + 1) per)
+  int tiles;
+  int pad[3];
+};
+
+struct SharedTables {
+  const SharedHead* head;     // null: no shared part
+  const SharedTile* tiles;
+  const int32_t* order;       // sequences, grouped by prefix
+  const int32_t* seq_tile;    // tile of sequence b (-1: it has no shared rows)
+  const int32_t* seq_row;     // its row there
+  float* records;             // [B * H + CTAs * kSharedRows][kRecordFloats]
+};
+
+struct BalancedArgs {
+  int B, H, n;
+  int64_t cap;
+  const uint16_t* q;
+  const uint16_t* pk;
+  const uint16_t* pv;
+  const int32_t* prefix_len;  // not read when cap == 0
+  const uint16_t* ring_k;
+  const uint16_t* ring_v;
+  const int32_t* wp;
+  const int32_t* fill;
+  float scale;
+  void* out;  // f32; bf16 with a shared part
+  float* lse;
+  int32_t* status;
+  // scored decode
+  float softcap;           // 0: none
+  const float* slopes;     // [H] or null
+  const int32_t* pos;      // [B], with slopes
+  const int2* ranges;      // [B] or null: the whole prefix
+  SharedTables shared;
+  // set by launch_balanced
+  int32_t* counters;
+  float* records;
+  int min_share;
+};
+
+int balanced_grid();
+size_t balanced_scratch_bytes();  // of launch_balanced's zero-filled scratch
+cudaError_t launch_balanced(BalancedArgs a, void* scratch, cudaStream_t stream);
+
+}  // namespace rswa

@@ -1,0 +1,697 @@
+// shared.cu -- the shared part of shared-prefix decode: many sequences, each with one query a
+// head, over few long prefixes that they have in common.
+//
+// Each shared key / value row is read once for up to 256 sequences instead of once a sequence:
+// the queries of a prefix's sequences are gathered into 128-row tiles and the products run on
+// the tensor cores (tcgen05, accumulators in TMEM), scores S = Q K^T and O += P V, P = exp(S - max)
+// rounded to bf16. What bounds it: at up to about 128 sequences a prefix the K / V bytes (64 KiB a
+// key tile of 128 rows, some 2,700 cycles of one SM's share of HBM, against 512 cycles of MMA
+// and about 1,000 of exponentials); above that the exponentials.
+//
+// group_kernel (one CTA): sorts the sequences by prefix, stably, so that a call's cut and with it
+// its rounding depend on the inputs alone, and lays the tables out. shared_kernel: one CTA an SM;
+// the work is a line of units (a key tile of one head of one tile of sequences) cut evenly over the
+// CTAs, so few long prefixes fill the chip as well as many short ones. A CTA walks its run in
+// segments, one per (tile, head), with roles as in the chunked prefill:
+//   warp 0 / warp 2, lane 0 : TMA producers of the K / V tiles, running ahead across segments
+//   warp 1                  : issues the MMAs; zeroes V rows past the prefix's end (0 * NaN)
+//   warps 4-7, 8-11         : softmax groups A and B; thread r owns TMEM lane r of its group
+// With more than 128 sequences in the tile the groups take 128 rows each and read the same keys;
+// with fewer, both take the same rows and every other key tile, so that one group's exponentials
+// run under the other's MMAs, and meet at the segment's end. A segment leaves one record a row
+// (max, sum of the rounded weights, sum of the weights, f32 accumulator), which the launch that
+// attends to the private rows joins. Every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "balanced.h"
+#include "common.cuh"
+#include "internal.h"
+#include "shared.h"
+#include "tcgen05.cuh"
+
+namespace rswa {
+
+namespace {
+
+constexpr int kRows = 128;                 // rows of a query tile, keys of a key tile
+constexpr int kRegionBytes = kRows * 128;  // one 64-column 128-byte-swizzled region
+constexpr int kTileBytes = 2 * kRegionBytes;
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarp0 = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;
+constexpr float kLazyRescaleLog2 = 8.f;
+constexpr int kGroupThreads = 1024;
+
+// ---------------------------------------------------------------------------------------------
+// grouping
+// ---------------------------------------------------------------------------------------------
+
+struct GroupArgs {
+  int B, H, P;
+  int64_t cap;
+  int ctas;
+  const int32_t* shared_len;
+  const int32_t* share_of;
+  SharedHead* head;
+  SharedTile* tiles;
+  int32_t* order;
+  int32_t* seq_tile;
+  int32_t* seq_row;
+  int32_t* status;
+};
+
+// Exclusive scan of v over the block; total over all threads.
+template <typename V>
+__device__ V block_scan(V v, V* warps, V& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  V inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const V t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = inc;
+  __syncthreads();
+  V before = 0;
+  total = 0;
+  for (int w = 0; w < kGroupThreads / 32; ++w) {
+    const V x = warps[w];
+    before += w < warp ? x : 0;
+    total += x;
+  }
+  return before + inc - v;
+}
+
+__global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a) {
+  extern __shared__ int tab[];
+  int* count = tab;           // sequences of prefix p
+  int* first = tab + a.P;     // its first place in order[]
+  int* tile0 = tab + 2 * a.P;  // its first tile (-1: no rows, or nobody reads it)
+  __shared__ long long scan[kGroupThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int p = tid; p < a.P; p += kGroupThreads) count[p] = 0;
+  __syncthreads();
+  // each sequence's rank among its prefix's, in order of the sequences
+  for (int base = 0; base < a.B; base += kGroupThreads) {
+    const int b = base + tid;
+    int p = b < a.B ? a.share_of[b] : -1;
+    if (p < -1 || p >= a.P) {
+      set_status(a.status, RSWA_DEVICE_BAD_SHARE);
+      p = -1;
+    }
+    const unsigned same = __match_any_sync(0xffffffffu, p);
+    const int leader = __ffs(same) - 1;
+    int rank = 0;
+    const int warps = min(kGroupThreads / 32, (a.B - base + 31) / 32);
+    for (int w = 0; w < warps; ++w) {
+      if (warp == w && lane == leader && p >= 0) {
+        rank = count[p];
+        count[p] = rank + __popc(same);
+      }
+      __syncthreads();
+    }
+    rank = __shfl_sync(0xffffffffu, rank, leader) + __popc(same & ((1u << lane) - 1));
+    if (b < a.B) {
+      a.seq_tile[b] = p;
+      a.seq_row[b] = rank;
+    }
+  }
+  long long seqs = 0, tiles = 0, units = 0;  // so far
+  for (int base = 0; base < a.P; base += kGroupThreads) {
+    const int p = base + tid;
+    int n = p < a.P ? count[p] : 0;
+    int len = 0;
+    if (n > 0) {
+      len = a.shared_len[p];
+      if (len < 0 || len > a.cap) {
+        set_status(a.status, RSWA_DEVICE_BAD_PREFIX_LEN);
+        len = 0;
+      }
+      if (len == 0) n = 0;
+    }
+    const int nt = (n + kSharedRows - 1) / kSharedRows;
+    const int keys = (len + kRows - 1) / kRows;
+    const long long each = (long long)keys * a.H;
+    long long t_seqs, t_tiles, t_units;
+    const long long s0 = seqs + block_scan<long long>(n, scan, t_seqs);
+    const long long k0 = tiles + block_scan<long long>(nt, scan, t_tiles);
+    const long long u0 = units + block_scan<long long>(nt * each, scan, t_units);
+    if (p < a.P) {
+      first[p] = (int)s0;
+      tile0[p] = nt > 0 ? (int)k0 : -1;
+      for (int i = 0; i < nt; ++i) {
+        SharedTile t;
+        t.first_unit = u0 + i * each;
+        t.first_seq = (int)s0 + i * kSharedRows;
+        t.rows = min(kSharedRows, n - i * kSharedRows);
+        t.prefix = p;
+        t.len = len;
+        t.key_tiles = keys;
+        t.pad = 0;
+        a.tiles[k0 + i] = t;
+      }
+    }
+    seqs += t_seqs;
+    tiles += t_tiles;
+    units += t_units;
+  }
+  __syncthreads();
+  for (int b = tid; b < a.B; b += kGroupThreads) {  // the rows this thread wrote above
+    const int p = a.seq_tile[b], rank = a.seq_row[b];
+    const bool has = p >= 0 && tile0[p] >= 0;
+    if (has) a.order[first[p] + rank] = b;
+    a.seq_tile[b] = has ? tile0[p] + rank / kSharedRows : -1;
+    a.seq_row[b] = rank % kSharedRows;
+  }
+  if (tid == 0) {
+    a.head->units = units;
+    a.head->per = max(1ll, (units + a.ctas - 1) / a.ctas);
+    a.head->tiles = (int)tiles;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// attention
+// ---------------------------------------------------------------------------------------------
+
+struct SharedSmem {
+  uint8_t q[2][kTileBytes];
+  uint8_t k[kKStages][kTileBytes];
+  uint8_t v[kVStages][kTileBytes];
+  uint64_t q_full;
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  float stat_m[2][kRows];              // at a segment's end: both groups' maxima,
+  float stat_l[kRows], stat_lu[kRows];  // group B's sums
+};
+// the swizzled tiles need the struct at a 1,024-byte boundary, and there is no room to move it
+static_assert(sizeof(SharedSmem) <= 227 * 1024, "shared memory");
+
+struct AttnArgs {
+  int B, H;
+  int64_t cap;
+  const uint16_t* q;
+  float scale_log2;
+  SharedTables t;
+  int32_t* status;
+};
+
+__device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
+  if (*reinterpret_cast<volatile int*>(&sm.abort_flag)) return false;
+  if (mbar_wait(bar, parity)) return true;
+  sm.abort_flag = 1;
+  set_status(status, RSWA_DEVICE_WAIT_TIMEOUT);
+  return false;
+}
+
+// A CTA's run of units as segments: key tiles [k0, k1) of head h of one tile of sequences.
+struct Walk {
+  long long u, end;
+  int ti, h, k0, k1;
+  SharedTile t;
+
+  __device__ __forceinline__ bool begin(const SharedTables& tab) {
+    const long long per = tab.head->per, units = tab.head->units;
+    u = (long long)blockIdx.x * per;
+    end = min(u + per, units);
+    if (u >= end) return false;
+    int lo = 0, hi = tab.head->tiles - 1;  // the last tile whose first unit is at or before u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tab.tiles[mid].first_unit <= u)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    ti = lo;
+    t = tab.tiles[ti];
+    h = (int)((u - t.first_unit) / t.key_tiles);
+    k0 = (int)((u - t.first_unit) % t.key_tiles);
+    k1 = (int)min((long long)t.key_tiles, k0 + (end - u));
+    return true;
+  }
+  __device__ __forceinline__ bool next(const SharedTables& tab, int H) {
+    u += k1 - k0;
+    if (u >= end) return false;
+    if (++h == H) {
+      h = 0;
+      t = tab.tiles[++ti];
+    }
+    k0 = 0;
+    k1 = (int)min((long long)t.key_tiles, end - u);
+    return true;
+  }
+  __device__ __forceinline__ bool two() const { return t.rows > kRows; }  // a group takes its own rows
+  __device__ __forceinline__ int events() const { return two() ? 2 * (k1 - k0) : k1 - k0; }
+};
+
+// Both softmax groups meet; true for all of them if any thread gives up, so that they leave together.
+__device__ __forceinline__ bool softmax_barrier_or(bool stop) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(stop ? 1u : 0u)
+      : "memory");
+  return any != 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  SharedSmem& sm = *reinterpret_cast<SharedSmem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((smem_addr(smem_raw) & 1023u) != 0) {  // it is, with no other shared memory in the kernel
+    if (tid == 0) set_status(a.status, RSWA_DEVICE_PIPELINE);
+    return;
+  }
+  if (tid == 0) {
+    sm.abort_flag = 0;
+    mbar_init(&sm.q_full, 256);
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.s_full[x], 1);
+      mbar_init(&sm.p_full[x], 128);
+      mbar_init(&sm.o_done[x], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  griddep_wait();  // the tables come from the grouping launch
+  griddep_launch_dependents();
+
+  Walk w;
+  bool more = w.begin(a.t);
+  if (warp == 0 || warp == 2) {
+    // ---------------- producers: K tiles (warp 0), V tiles (warp 2) ----------------
+    if (lane == 0) {
+      const bool is_k = warp == 0;
+      const int stages = is_k ? kKStages : kVStages;
+      uint64_t* full = is_k ? sm.k_full : sm.v_full;
+      uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+      int n = 0;  // tiles issued
+      bool ok = true;
+      for (; ok && more; more = w.next(a.t, a.H)) {
+        const int row0 = (int)(((int64_t)w.t.prefix * a.H + w.h) * a.cap);
+        for (int k = w.k0; k < w.k1; ++k, ++n) {
+          const int s = n % stages;
+          if (n >= stages && !wait_or_abort(sm, &empty[s], ((n / stages) - 1) & 1, a.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = is_k ? sm.k[s] : sm.v[s];
+          mbar_arrive_expect_tx(&full[s], kTileBytes);
+          tma_load_2d(dst, map, 0, row0 + k * kRows, &full[s]);
+          tma_load_2d(dst + kRegionBytes, map, 64, row0 + k * kRows, &full[s]);
+        }
+      }
+      if (sm.abort_flag)  // let the copies in flight land before shared memory is released
+        for (int i = max(0, n - stages); i < n; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (lane 0), V-row zeroing (whole warp) ----------------
+    constexpr uint32_t kIdescQK = idesc_bf16_m128_n128(0);
+    constexpr uint32_t kIdescPV = idesc_bf16_m128_n128(1);
+    int base = 0;             // key tiles before this segment
+    uint32_t n_p[2] = {0, 0};  // P tiles consumed of each group
+    bool ok = true;
+    for (int seg = 0; ok && more; more = w.next(a.t, a.H), ++seg) {
+      const bool two = w.two();
+      const int events = w.events();
+      int k_seen = -1, v_seen = -1;  // tiles of this segment that were waited for
+      ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.q_full, seg & 1, a.status));
+      if (!ok) break;
+      tc_fence_after();
+      auto issue_s = [&](int e) {
+        const int x = e & 1, t = two ? e >> 1 : e, n = base + t, s = n % kKStages;
+        if (t > k_seen) {
+          if (!__all_sync(0xffffffffu, wait_or_abort(sm, &sm.k_full[s], (n / kKStages) & 1, a.status))) return false;
+          tc_fence_after();
+          k_seen = t;
+        }
+        if (lane == 0) {
+          const uint32_t q_addr = smem_addr(sm.q[two ? x : 0]);
+          const uint32_t k_addr = smem_addr(sm.k[s]);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (uint32_t)(kk >> 2) * kRegionBytes + (uint32_t)(kk & 3) * 32u;
+            tc_mma_ss(tmem + (uint32_t)x * 128u, smem_desc_sw128(q_addr + off, 16, 1024),
+                      smem_desc_sw128(k_addr + off, 16, 1024), kIdescQK, kk > 0);
+          }
+          tc_commit(&sm.s_full[x]);
+          if (!two || x == 1) tc_commit(&sm.k_empty[s]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int e = 0; ok && e < min(2, events); ++e) ok = issue_s(e);
+      for (int e = 0; ok && e < events; ++e) {
+        const int x = e & 1, t = two ? e >> 1 : e, n = base + t, s = n % kVStages;
+        if (t > v_seen) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[s], (n / kVStages) & 1, a.status));
+          if (!ok) break;
+          v_seen = t;
+          const int left = w.t.len - (w.k0 + t) * kRows;  // rows of the prefix in this tile
+          if (left < kRows) {
+            for (int r = left + lane; r < kRows; r += 32) {
+              uint4* row0 = reinterpret_cast<uint4*>(sm.v[s] + r * 128);
+              uint4* row1 = reinterpret_cast<uint4*>(sm.v[s] + kRegionBytes + r * 128);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                row0[i] = make_uint4(0, 0, 0, 0);
+                row1[i] = make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_async_smem();
+            __syncwarp();
+          }
+        }
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.p_full[x], n_p[x] & 1, a.status));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t v_addr = smem_addr(sm.v[s]);
+          const uint32_t p_tmem = tmem + (uint32_t)x * 128u;
+          const uint32_t o_tmem = tmem + kColO + (uint32_t)x * 128u;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_ts(o_tmem, p_tmem + (uint32_t)kk * 8u, smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, kRegionBytes, 1024),
+                      kIdescPV, (e > 1 || kk > 0) ? 1u : 0u);
+          tc_commit(&sm.o_done[x]);
+          if (!two || x == 1) tc_commit(&sm.v_empty[s]);
+        }
+        __syncwarp();
+        ++n_p[x];
+        if (e + 2 < events) ok = issue_s(e + 2);
+      }
+      base += w.k1 - w.k0;
+    }
+    if (lane == 0) tc_commit(&sm.drain);  // fires once every issued MMA is done
+  } else if (warp >= kSoftmaxWarp0) {
+    // ---------------- softmax groups ----------------
+    const int x = (warp - kSoftmaxWarp0) / 4;
+    const int r = tid - (kSoftmaxWarp0 + 4 * x) * 32;
+    const uint32_t lane_base = (uint32_t)(((warp - kSoftmaxWarp0) & 3) * 32) << 16;
+    const uint32_t s_cols = tmem + lane_base + (uint32_t)x * 128u;
+    const uint32_t o_cols = tmem + lane_base + kColO;  // O of group A; B's is 128 columns on
+    uint32_t seen = 0;  // scores of this group so far, over all segments
+    bool ok = true;
+    for (; ok && more; more = w.next(a.t, a.H)) {
+      const bool two = w.two();
+      const int row = two ? x * kRows + r : r;
+      const bool live = row < w.t.rows;
+      const bool warp_live = (two ? x * kRows : 0) + (r & ~31) < w.t.rows;
+      {  // this segment's queries into shared memory, 128-byte swizzled
+        uint4 z = make_uint4(0, 0, 0, 0);
+        const uint4* src = nullptr;
+        if (live)
+          src = reinterpret_cast<const uint4*>(a.q + ((int64_t)a.t.order[w.t.first_seq + row] * a.H + w.h) * kHeadDim);
+        // two tiles: a thread copies its row; one tile: groups A and B copy a row's halves
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!two && half != x) continue;
+          uint8_t* dst = sm.q[two ? x : 0] + half * kRegionBytes + r * 128;
+          uint4 buf[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) buf[i] = src != nullptr ? src[half * 8 + i] : z;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + ((i ^ (r & 7)) << 4)) = buf[i];
+        }
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(&sm.q_full);
+      }
+      float m_used = -INFINITY, l = 0.f, lu = 0.f;
+      const int events = w.events();
+      for (int e = x; e < events; e += 2) {
+        const int t = two ? e >> 1 : e;
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], seen & 1, a.status));
+        if (!ok) break;
+        tc_fence_after();
+        ++seen;
+        if (warp_live) {
+          const int left = w.t.len - (w.k0 + t) * kRows;
+          const bool full = left >= kRows;
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t rr[32];
+            tmem_ld32(s_cols + (uint32_t)ch * 32u, rr);
+            tmem_wait_ld();
+            if (full) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                m0 = max3(m0, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
+                m1 = max3(m1, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (ch * 32 + i < left) m0 = fmaxf(m0, __uint_as_float(rr[i]));
+            }
+          }
+          const float tmax = fmaxf(m0, m1) * a.scale_log2;
+          const bool rescale = tmax > m_used + kLazyRescaleLog2;
+          float alpha = 1.f;
+          if (rescale) {
+            alpha = ex2(m_used - tmax);
+            l *= alpha;
+            lu *= alpha;
+            m_used = tmax;
+          }
+          // the previous P V of this group is done (the commit that completed S covers it)
+          if (e >= 2 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t rr[32];
+              tmem_ld32(o_cols + (uint32_t)(x * 128 + ch * 32), rr);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * alpha);
+              tmem_st32(o_cols + (uint32_t)(x * 128 + ch * 32), rr);
+            }
+          }
+          const float m_sub = m_used == -INFINITY ? 0.f : m_used;
+          float2 ls = make_float2(0.f, 0.f), lus = make_float2(0.f, 0.f);
+          const float2 neg_m = make_float2(-m_sub, -m_sub);
+          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t rr[32];
+            tmem_ld32(s_cols + (uint32_t)ch * 32u, rr);
+            tmem_wait_ld();
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 z2 = __ffma2_rn(make_float2(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1])), scale2,
+                                           neg_m);
+              float2 p2 = make_float2(ex2(z2.x), ex2(z2.y));
+              if (!full) {
+                if (ch * 32 + 2 * i >= left) p2.x = 0.f;
+                if (ch * 32 + 2 * i + 1 >= left) p2.y = 0.f;
+              }
+              const __nv_bfloat162 pb = __floats2bfloat162_rn(p2.x, p2.y);
+              pk[i] = *reinterpret_cast<const uint32_t*>(&pb);
+              ls = __fadd2_rn(ls, make_float2(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u)));
+              lus = __fadd2_rn(lus, p2);
+            }
+            tmem_st16(s_cols + (uint32_t)ch * 16u, pk);
+          }
+          l += ls.x + ls.y;
+          lu += lus.x + lus.y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[x]);
+      }
+      // ---- the segment's records ----
+      const bool any = x < events;
+      if (ok && any) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (seen - 1) & 1, a.status));
+      if (!two) {
+        sm.stat_m[x][r] = m_used;
+        if (x == 1) {
+          sm.stat_l[r] = l;
+          sm.stat_lu[r] = lu;
+        }
+      }
+      tc_fence_before();
+      if (softmax_barrier_or(!ok)) break;
+      tc_fence_after();
+      if (warp_live) {
+        // the run that holds the tile's first keys, or this CTA's (it began inside)
+        float* rec = a.t.records + (w.k0 == 0 ? (int64_t)w.t.first_seq * a.H + (int64_t)w.h * w.t.rows + row
+                                              : (int64_t)a.B * a.H + (int64_t)blockIdx.x * kSharedRows + row) *
+                                       kRecordFloats;
+        if (two) {
+          if (live) *reinterpret_cast<float4*>(rec) = make_float4(m_used, l, lu, 0.f);
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t rr[32];
+            tmem_ld32(o_cols + (uint32_t)(x * 128 + ch * 32), rr);
+            tmem_wait_ld();
+            if (live)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(rec + 4 + ch * 32 + i) =
+                    make_float4(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1]), __uint_as_float(rr[i + 2]),
+                                __uint_as_float(rr[i + 3]));
+          }
+        } else {
+          // the two groups' halves of the keys meet; each writes half of the columns
+          const bool both = events > 1;
+          const float ma = sm.stat_m[0][r], mb = sm.stat_m[1][r];
+          const float M = fmaxf(ma, mb), m_sub = M == -INFINITY ? 0.f : M;
+          const float fa = ex2(ma - m_sub), fb = both ? ex2(mb - m_sub) : 0.f;
+          if (live && x == 0)
+            *reinterpret_cast<float4*>(rec) =
+                make_float4(M, fmaf(sm.stat_l[r], fb, l * fa), fmaf(sm.stat_lu[r], fb, lu * fa), 0.f);
+#pragma unroll 1
+          for (int ch = 0; ch < 2; ++ch) {
+            const uint32_t col = (uint32_t)(x * 64 + ch * 32);
+            uint32_t ra[32], rb[32];
+            tmem_ld32(o_cols + col, ra);
+            if (both) tmem_ld32(o_cols + 128u + col, rb);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float o = __uint_as_float(ra[i]) * fa;
+              if (both) o = fmaf(__uint_as_float(rb[i]), fb, o);
+              ra[i] = __float_as_uint(o);
+            }
+            if (live)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(rec + 4 + col + i) =
+                    make_float4(__uint_as_float(ra[i]), __uint_as_float(ra[i + 1]), __uint_as_float(ra[i + 2]),
+                                __uint_as_float(ra[i + 3]));
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    if (lane == 0) mbar_wait(&sm.drain, 0);  // bounded; the MMAs drain before their TMEM is freed
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+int64_t most_tiles(int B, int P) {
+  // every prefix can leave one tile part full, and each tile has at least one sequence
+  const int64_t t = (int64_t)P + B / kSharedRows;
+  return t < B ? t : B;
+}
+
+}  // namespace
+
+SharedPlan plan_shared(int B, int H, int P) {
+  SharedPlan p;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  p.head = take(sizeof(SharedHead));
+  p.tiles = take((size_t)most_tiles(B, P) * sizeof(SharedTile));
+  p.order = take((size_t)B * 4);
+  p.seq_tile = take((size_t)B * 4);
+  p.seq_row = take((size_t)B * 4);
+  p.records = take(((size_t)B * H + (size_t)device_sm_count() * kSharedRows) * kRecordFloats * 4);
+  p.bytes = off;
+  return p;
+}
+
+cudaError_t launch_shared(const SharedLaunch& L, void* scratch, SharedTables* tables, cudaStream_t stream) {
+  const SharedPlan p = plan_shared(L.B, L.H, L.P);
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  const int ctas = device_sm_count();
+  GroupArgs g;
+  g.B = L.B;
+  g.H = L.H;
+  g.P = L.P;
+  g.cap = L.cap;
+  g.ctas = ctas;
+  g.shared_len = L.shared_len;
+  g.share_of = L.share_of;
+  g.head = reinterpret_cast<SharedHead*>(base + p.head);
+  g.tiles = reinterpret_cast<SharedTile*>(base + p.tiles);
+  g.order = reinterpret_cast<int32_t*>(base + p.order);
+  g.seq_tile = reinterpret_cast<int32_t*>(base + p.seq_tile);
+  g.seq_row = reinterpret_cast<int32_t*>(base + p.seq_row);
+  g.status = L.status;
+  static unsigned long long done[2] = {};
+  cudaError_t e;
+  const size_t tab = (size_t)L.P * 12;
+  if ((e = ensure_smem_limit(group_kernel, (size_t)kMaxShared * 12, &done[0])) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  fill_launch_config(cfg, attr, dim3(1), dim3(kGroupThreads), tab, stream);
+  if ((e = cudaLaunchKernelEx(&cfg, group_kernel, g)) != cudaSuccess) return e;
+
+  tables->head = g.head;
+  tables->tiles = g.tiles;
+  tables->order = g.order;
+  tables->seq_tile = g.seq_tile;
+  tables->seq_row = g.seq_row;
+  tables->records = reinterpret_cast<float*>(base + p.records);
+  AttnArgs a;
+  a.B = L.B;
+  a.H = L.H;
+  a.cap = L.cap;
+  a.q = L.q;
+  a.scale_log2 = L.scale * 1.4426950408889634f;
+  a.t = *tables;
+  a.status = L.status;
+  CUtensorMap tk, tv;
+  const int64_t rows = (int64_t)L.P * L.H * L.cap;
+  if ((e = make_rows_map(&tk, L.sk, rows)) != cudaSuccess) return e;
+  if ((e = make_rows_map(&tv, L.sv, rows)) != cudaSuccess) return e;
+  const size_t smem = sizeof(SharedSmem);
+  if ((e = ensure_smem_limit(shared_kernel, smem, &done[1])) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg2 = {};
+  cudaLaunchAttribute attr2[1];
+  fill_launch_config(cfg2, attr2, dim3(ctas), dim3(kThreads), smem, stream);
+  return cudaLaunchKernelEx(&cfg2, shared_kernel, a, tk, tv);
+}
+
+}  // namespace rswa

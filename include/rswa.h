@@ -83,7 +83,7 @@ typedef struct {
 #define RSWA_OP_SRSWA_DECODE 2  /* srswa_decode, srswa_decode_fp8, srswa_decode_append
                                    (any topk in 1..32)                                      */
 #define RSWA_OP_ROUTE 3         /* srswa_route, srswa_route_tokens (256 bytes)               */
-#define RSWA_OP_PREFILL 4       /* rswa_prefill (256 bytes); srswa_prefill: srswa_prefill_workspace_bytes */
+#define RSWA_OP_PREFILL 4       /* rswa_prefill, rswa_prefill_scored (256 bytes); srswa_prefill: srswa_prefill_workspace_bytes */
 #define RSWA_OP_SRSWA_ROUTED 5  /* srswa_decode_routed, srswa_step (any topk in 1..32)       */
 #define RSWA_OP_DECODE_SCORED 6 /* rswa_decode_scored                                        */
 
@@ -623,6 +623,27 @@ RSWA_API rswa_status rswa_decode_scored(const rswa_dims* dims, const rswa_score*
                                         const void* pv, const int32_t* prefix_len, const void* ring_k,
                                         const void* ring_v, const int32_t* wp, const int32_t* fill, float scale,
                                         float* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * R-SWA chunked prefill with the scores of rswa_decode_scored: query i of the chunk attends to
+ * the prefix rows [lo, hi) of its own document, to the chunk's outputs j with i - n < j <= i and,
+ * for j < 0, to the ring, as rswa_prefill does. Query i stands at position pos[b] + i (pos: of the
+ * chunk's first query), output j at pos[b] + j, prefix row x at x.
+ * Arguments as rswa_prefill, with
+ *   score : slope and pos as in rswa_decode_scored; range : int32 [batch][T][2] or NULL, one
+ *           document a query
+ *   out   : bf16 [B][H][T][D] (P is rounded to bf16 for P V, and more bits would carry nothing);
+ *           lse : f32 [B][H][T] or NULL, from unrounded weights
+ * Prefix tiles of 128 rows that no query of a 256-query tile sees are skipped. Prefix rows that no
+ * query of such a tile sees, and rows past a length, may hold anything; a non-finite row that
+ * some query of the tile sees can reach the tile's other queries.
+ * prefix_cap may be 0 (pk, pv and prefix_len are then not read).
+ */
+RSWA_API rswa_status rswa_prefill_scored(const rswa_dims* dims, const rswa_score* score, int32_t T, const void* q,
+                                         const void* k_out, const void* v_out, const void* pk, const void* pv,
+                                         const int32_t* prefix_len, void* ring_k, void* ring_v, int32_t* wp,
+                                         int32_t* fill, float scale, void* out, float* lse, int32_t write_ring,
+                                         void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * R-SWA decode of sequences that share prefixes: sequence b attends to the rows

@@ -13,7 +13,8 @@ from .binding import (  # noqa: F401
     srswa_route,
     srswa_route_tokens, test_arm_wait_timeout, workspace_bytes, srswa_decode_routed, srswa_step,
     srswa_prefill_workspace, rswa_decode_append_rope, srswa_step_rope, rswa_rope_1d,
-    OP_DECODE_SCORED, new_shared_workspace, rswa_decode_scored, rswa_decode_shared, shared_workspace_bytes,
+    OP_DECODE_SCORED, new_shared_workspace, rswa_decode_scored, rswa_decode_shared, rswa_prefill_scored,
+    shared_workspace_bytes,
 )
 from .rotary import rope_freqs  # noqa: F401
 
@@ -23,5 +24,5 @@ __all__ = ["load", "Dims", "RswaError", "rswa_append", "rswa_decode", "rswa_pref
            "rswa_rope_page2d", "rswa_append_rope", "rswa_append_fp8", "rswa_decode_fp8kv", "srswa_decode_fp8kv",
            "fp8_ring_buffers", "test_arm_wait_timeout", "srswa_decode_routed", "srswa_step",
            "srswa_prefill_workspace", "rswa_decode_append_rope", "srswa_step_rope", "rswa_rope_1d", "rope_freqs",
-           "rswa_decode_scored", "rswa_decode_shared", "new_shared_workspace", "shared_workspace_bytes",
+           "rswa_decode_scored", "rswa_prefill_scored", "rswa_decode_shared", "new_shared_workspace", "shared_workspace_bytes",
            "workspace_bytes", "new_workspace", "route_workspace", "check_status", "dims_of"]

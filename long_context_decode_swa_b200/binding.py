@@ -45,7 +45,7 @@ EXPORTED = ("rswa_last_error", "rswa_version", "rswa_workspace_bytes", "rswa_che
             "rswa_decode_append", "srswa_decode_append", "rswa_rope_page2d", "rswa_append_rope", "rswa_append_fp8",
             "rswa_decode_fp8kv", "srswa_decode_fp8kv", "rswa_test_arm_wait_timeout", "srswa_decode_routed",
             "srswa_step", "srswa_prefill_workspace_bytes", "rswa_decode_append_rope", "srswa_step_rope", "rswa_rope_1d",
-            "rswa_decode_scored", "rswa_decode_shared", "rswa_decode_shared_workspace_bytes")
+            "rswa_decode_scored", "rswa_prefill_scored", "rswa_decode_shared", "rswa_decode_shared_workspace_bytes")
 
 
 class RswaError(RuntimeError):
@@ -147,6 +147,8 @@ def load(path: str | None = None):
         sig["rswa_rope_1d"] = ([ctypes.POINTER(Rope1d), P, P, P, P, P, P, P], ctypes.c_int)
         sig["rswa_decode_scored"] = ([DP, ctypes.POINTER(Score), P, P, P, P, P, P, P, P, F32, P, P, P, SZ, P],
                                      ctypes.c_int)
+        sig["rswa_prefill_scored"] = ([DP, ctypes.POINTER(Score), I32, P, P, P, P, P, P, P, P, P, P, F32, P, P, I32, P,
+                                       SZ, P], ctypes.c_int)
         sig["rswa_decode_shared_workspace_bytes"] = ([DP, I32], SZ)
         sig["rswa_decode_shared"] = ([DP, I32, I64, P, P, P, P, P, P, P, P, P, P, P, P, F32, P, P, P, SZ, P],
                                      ctypes.c_int)
@@ -988,6 +990,37 @@ def rswa_decode_scored(q, pk, pv, prefix_len, ring_k, ring_v, wp, fill, out, wor
           _tensor(prefix_len, "prefix_len", i32, (B,), dev), rk, rv, w, f,
           1.0 / math.sqrt(D) if scale is None else scale, _tensor(out, "out", f32, (B, H, D), dev),
           None if lse is None else _tensor(lse, "lse", f32, (B, H), dev), wsp, wsn)
+
+
+def rswa_prefill_scored(q, k_out, v_out, pk, pv, prefix_len, out, workspace, softcap: float = 0.0, slopes=None,
+                        pos=None, ranges=None, lse=None, ring_k=None, ring_v=None, wp=None, fill=None,
+                        write_ring=False, scale=None, ring: int | None = None, stream=None):
+    """Chunked R-SWA prefill with the scores of rswa_decode_scored. q/k_out/v_out bf16 [B][H][T][D]; slopes
+    f32 [H] with pos int32 [B] (the position of the chunk's first query); ranges int32 [B][T][2], each
+    query's document in the prefix; out bf16 [B][H][T][D], lse f32 [B][H][T]. Ring arguments as in
+    rswa_prefill. workspace: new_workspace(dims, OP_PREFILL)."""
+    dev = _device_of(q, "q")
+    if q.dim() != 4 or not isinstance(pk, torch.Tensor) or pk.dim() != 4:
+        raise ValueError("expected q [B, H, T, D] and pk [B, H, cap, D]")
+    B, H, T, D = q.shape
+    cap = pk.shape[2]
+    bf16, i32 = torch.bfloat16, torch.int32
+    rk = rv = w = f = None
+    if ring_k is not None:
+        rk, rv, w, f = _ring(ring_k, ring_v, wp, fill, B, H, D, dev)
+        n = ring_k.shape[2]
+    else:
+        if ring is None:
+            raise ValueError("without a ring tensor, pass the window length as ring=n")
+        n = int(ring)
+    score = _score(softcap, slopes, pos, ranges, H, (B, T), dev)
+    wsp, wsn = _workspace(workspace, dev)
+    _call("rswa_prefill_scored", dev, stream, Dims(B, H, D, n, cap), score, T, _tensor(q, "q", bf16, (B, H, T, D), dev),
+          _tensor(k_out, "k_out", bf16, (B, H, T, D), dev), _tensor(v_out, "v_out", bf16, (B, H, T, D), dev),
+          _tensor(pk, "pk", bf16, (B, H, cap, D), dev), _tensor(pv, "pv", bf16, (B, H, cap, D), dev),
+          _tensor(prefix_len, "prefix_len", i32, (B,), dev), rk, rv, w, f, 1.0 / math.sqrt(D) if scale is None else scale,
+          _tensor(out, "out", bf16, (B, H, T, D), dev),
+          None if lse is None else _tensor(lse, "lse", torch.float32, (B, H, T), dev), 1 if write_ring else 0, wsp, wsn)
 
 
 def shared_workspace_bytes(dims: Dims, n_shared: int) -> int:

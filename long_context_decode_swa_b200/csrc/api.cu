@@ -14,6 +14,7 @@
 #include "balanced.h"
 #include "common.cuh"
 #include "internal.h"
+#include "scored_prefill.h"
 #include "shared.h"
 
 namespace {
@@ -1169,6 +1170,76 @@ rswa_status rswa_decode_scored(const rswa_dims* dims, const rswa_score* score, c
   a.ranges = reinterpret_cast<const int2*>(score->range);
   cudaError_t e =
       rswa::launch_balanced(a, static_cast<uint8_t*>(workspace) + 256, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+rswa_status rswa_prefill_scored(const rswa_dims* dims, const rswa_score* score, int32_t T, const void* q,
+                                const void* k_out, const void* v_out, const void* pk, const void* pv,
+                                const int32_t* prefix_len, void* ring_k, void* ring_v, int32_t* wp, int32_t* fill,
+                                float scale, void* out, float* lse, int32_t write_ring, void* workspace,
+                                size_t ws_bytes, void* stream) {
+  const char* fn = "rswa_prefill_scored";
+  const NvtxRange nvtx_range(fn);
+  rswa_status st = check_dims(fn, dims, true);
+  if (st != RSWA_OK) return st;
+  if ((st = check_score(fn, score)) != RSWA_OK) return st;
+  if (T < 1) return fail(RSWA_ERR_INVALID, "%s: T must be >= 1 (got %d)", fn, T);
+  REQUIRE_PTR(q);
+  REQUIRE_PTR(k_out);
+  REQUIRE_PTR(v_out);
+  REQUIRE_PTR(out);
+  REQUIRE_PTR(workspace);
+  REQUIRE_PTR_OR_NULL(lse);
+  if (dims->prefix_cap > 0) {
+    REQUIRE_PTR(pk);
+    REQUIRE_PTR(pv);
+    if (prefix_len == nullptr) return fail(RSWA_ERR_INVALID, "%s: prefix_len must not be NULL", fn);
+  }
+  const bool ring = ring_k != nullptr || ring_v != nullptr || wp != nullptr || fill != nullptr;
+  if (ring) {
+    REQUIRE_PTR(ring_k);
+    REQUIRE_PTR(ring_v);
+    if (wp == nullptr || fill == nullptr) return fail(RSWA_ERR_INVALID, "%s: a ring needs wp and fill", fn);
+  } else if (write_ring) {
+    return fail(RSWA_ERR_INVALID, "%s: write_ring needs a ring", fn);
+  }
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RSWA_ERR_INVALID, "%s: scale must be finite and > 0", fn);
+  if (ws_bytes < 256) return fail(RSWA_ERR_INVALID, "%s: workspace must be at least 256 bytes", fn);
+  const int64_t bh = (int64_t)dims->batch * dims->heads;
+  const int64_t lim = ((int64_t)1 << 31) - 1;
+  if (bh * T >= lim || bh * dims->prefix_cap >= lim || bh * dims->ring >= lim)
+    return fail(RSWA_ERR_UNSUPPORTED, "%s: more than 2^31 rows in one operand", fn);
+  rswa::ScoredPrefillLaunch L;
+  L.B = dims->batch;
+  L.H = dims->heads;
+  L.n = dims->ring;
+  L.T = T;
+  L.cap = dims->prefix_cap;
+  L.q = q;
+  L.k_out = k_out;
+  L.v_out = v_out;
+  L.pk = pk;
+  L.pv = pv;
+  L.prefix_len = prefix_len;
+  L.ring_k = ring ? ring_k : nullptr;
+  L.ring_v = ring ? ring_v : nullptr;
+  L.wp = wp;
+  L.fill = fill;
+  L.scale = scale;
+  L.softcap = score->softcap;
+  L.slopes = score->slope;
+  L.pos = score->pos;
+  L.ranges = reinterpret_cast<const int2*>(score->range);
+  L.out = out;
+  L.lse = lse;
+  L.write_ring = write_ring;
+  L.ring_k_w = ring_k;
+  L.ring_v_w = ring_v;
+  L.wp_w = wp;
+  L.fill_w = fill;
+  L.status = ws_status(workspace);
+  cudaError_t e = rswa::launch_scored_prefill(L, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
 }

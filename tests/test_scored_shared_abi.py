@@ -92,3 +92,28 @@ def test_workspace_sizes():
         rswa.shared_workspace_bytes(DIMS, 0)
     # one record a (sequence, head) and 256 a CTA, of 132 floats
     assert shared >= 2 * 4 * 132 * 4
+
+
+def _prefill(**kw):
+    lib = rswa.load()
+    a = dict(dims=DIMS, score=Score(30.0, None, None, None), T=16, q=A, k_out=A, v_out=A, pk=A, pv=A, prefix_len=A,
+             ring_k=A, ring_v=A, wp=A, fill=A, scale=0.088, out=A, lse=None, write_ring=0, ws=A, ws_bytes=256)
+    a.update(kw)
+    ref = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
+    code = lib.rswa_prefill_scored(ref(a["dims"]), ref(a["score"]), a["T"], a["q"], a["k_out"], a["v_out"], a["pk"],
+                                   a["pv"], a["prefix_len"], a["ring_k"], a["ring_v"], a["wp"], a["fill"], a["scale"],
+                                   a["out"], a["lse"], a["write_ring"], a["ws"], a["ws_bytes"], None)
+    return code, _err()
+
+
+@pytest.mark.parametrize("kw,code,word", COMMON + [
+    (dict(score=None), INVALID, "score"), (dict(score=Score(-0.5, None, None, None)), INVALID, "softcap"),
+    (dict(score=Score(0.0, 0x10000, None, None)), INVALID, "slope and pos"),
+    (dict(score=Score(0.0, None, None, 0x10004)), INVALID, "range"), (dict(T=0), INVALID, "T must"),
+    (dict(k_out=None), INVALID, "k_out"), (dict(v_out=MIS), INVALID, "aligned"), (dict(lse=MIS), INVALID, "aligned"),
+    (dict(ring_k=None, ring_v=None, wp=None, fill=None, write_ring=1), INVALID, "write_ring"),
+    (dict(T=2 ** 29), UNSUPPORTED, "2^31"), (dict(dims=Dims(64, 64, 128, 128, 2 ** 20)), UNSUPPORTED, "2^31"),
+])
+def test_prefill_scored_refusals(kw, code, word):
+    got, msg = _prefill(**kw)
+    assert got == code and word in msg, (got, msg)

@@ -571,7 +571,7 @@ RSWA_API rswa_status srswa_step_rope(const rswa_dims* dims, const rswa_rope* rop
  *   pos      : int32 [batch][tokens], any values
  *   q_out / k_out may be q / k with the same strides (in place; dims from rot_dim on are then
  *   not touched); other overlaps of an output with an input are not supported.
- * Arithmetic: the angle as a 64-bit fixed-point fraction of a turn (error below 2^-31 turns
+ * Arithmetic: the angle as a 64-bit fixed-point fraction of a turn (error below 2^-31 max(1, |inv_freq|) turns
  * for every int32 position), cos / sin and the rotation in f32, one rounding to bf16: within
  * 2^-20 (|x| + |y|) |mscale| plus half a bf16 step of the exact rotation by the table's angles.
  */

@@ -9,6 +9,7 @@ fallback: if the library is missing, ``load()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -191,6 +192,11 @@ def _want(t: torch.Tensor, name: str, dtype, shape=None):
 
 def _tensor(t, name: str, dtype, shape, device):
     """A contiguous tensor of this dtype and shape on `device`: its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype is not dtype:
@@ -199,9 +205,7 @@ def _tensor(t, name: str, dtype, shape, device):
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _device_of(t, name: str):
@@ -212,17 +216,27 @@ def _device_of(t, name: str):
     return t.device
 
 
+# The raw handle of a device's current stream, without building a torch.cuda.Stream (2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_fns: dict = {}
+
+
 def _call(name: str, device, stream, *args):
     """The C call on `stream` (default: the current stream of the tensors' device), with that device current."""
-    lib = load()
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(load(), name)
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == device.index:
-        code = getattr(lib, name)(*args, raw)
+        raw = _raw_stream(index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == index:
+        code = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            code = getattr(lib, name)(*args, raw)
+            code = fn(*args, raw)
     if code != 0:
         _check(name, code)
 
@@ -307,24 +321,35 @@ def rswa_rope_page2d(q, tok_pos, page, q_out=None, k=None, k_out=None, base: flo
     return q_out, k_out
 
 
-def _rope_rows(t, name: str, dtype, lead, device):
-    """(address, (batch, head, token) strides) of rows [B][H][T][D] or [B][H][D] in any order of their axes."""
+def _rope_rows(t, name: str, dtype, shape, device):
+    """The address of rows [B][H][T][D] or [B][H][D] in any order of their axes, the last one dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    if lead is not None and t.shape != lead:
-        raise ValueError(f"{name}: expected shape {tuple(lead)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last axis must be dense")
-    return t.data_ptr(), (st[0], st[1], st[2] if len(st) == 4 else 0)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_desc(dtype, layout, mscale, inverse, pairs, shape, heads_k, *strides):
+    """The descriptor of a call's shapes and strides (read-only)."""
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout: expected 'half' or 'interleaved', got {layout!r}")
+    d = Rope1d(shape[0], shape[1], heads_k, shape[2] if len(shape) == 4 else 1, shape[-1], 2 * pairs,
+               _ROPE_LAYOUTS[layout], _ROPE_DTYPES[dtype], 1 if inverse else 0, mscale)
+    for st, name in zip(strides, ("q", "q_out", "k", "k_out")):
+        if st[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"{name}: the last axis must be dense")
+        getattr(d, name + "_stride")[:] = (st[0], st[1], st[2] if len(st) == 4 else 0)
+    return d
 
 
 def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str = "half", mscale: float = 1.0,
@@ -336,38 +361,39 @@ def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str =
     through. layout: "half" or "interleaved" pairs. inverse=True applies the transpose, which turns
     gradients back. Outputs default to in place. Returns (q_out, k_out)."""
     dev = _device_of(q, "q")
-    if q.dim() not in (3, 4):
+    shape, dtype = q.shape, q.dtype
+    if len(shape) not in (3, 4):
         raise ValueError("q: expected [B, H, T, D] or [B, H, D]")
-    if q.dtype not in _ROPE_DTYPES:
-        raise TypeError(f"q: expected torch.bfloat16 or torch.float32, got {q.dtype}")
-    if layout not in _ROPE_LAYOUTS:
-        raise ValueError(f"layout: expected 'half' or 'interleaved', got {layout!r}")
+    if dtype not in _ROPE_DTYPES:
+        raise TypeError(f"q: expected torch.bfloat16 or torch.float32, got {dtype}")
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.is_cuda or inv_freq.dtype is not torch.float64 or \
             inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq: expected a contiguous 1-D float64 tensor on the CPU")
-    B, T = q.shape[0], (q.shape[2] if q.dim() == 4 else 1)
-    d = Rope1d(B, q.shape[1], 0, T, q.shape[-1], 2 * inv_freq.shape[0], _ROPE_LAYOUTS[layout], _ROPE_DTYPES[q.dtype],
-               1 if inverse else 0, mscale)
-    qp, d.q_stride[:] = _rope_rows(q, "q", q.dtype, None, dev)
-    q_out = q if q_out is None else q_out
-    qop, d.q_out_stride[:] = _rope_rows(q_out, "q_out", q.dtype, q.shape, dev)
-    kp = kop = None
-    if k is not None:
-        shape = (B, k.shape[1]) + tuple(q.shape[2:]) if isinstance(k, torch.Tensor) and k.dim() == q.dim() else q.shape
-        kp, d.k_stride[:] = _rope_rows(k, "k", q.dtype, shape, dev)
-        k_out = k if k_out is None else k_out
-        kop, d.k_out_stride[:] = _rope_rows(k_out, "k_out", q.dtype, k.shape, dev)
-        d.heads_k = k.shape[1]
-        if d.heads_k == 0:
-            raise ValueError("k: has no heads (pass None)")
-    elif k_out is not None:
-        raise ValueError("k_out given without k")
-    for src, dst, si, so, name in ((qp, qop, d.q_stride, d.q_out_stride, "q_out"),
-                                   (kp, kop, d.k_stride, d.k_out_stride, "k_out")):
-        if src is not None and src == dst and si[:] != so[:]:
-            raise ValueError(f"{name}: in place needs the input's strides")
-    _call("rswa_rope_1d", dev, stream, d, inv_freq.data_ptr(),
-          _tensor(pos, "pos", torch.int32, (B, T) if q.dim() == 4 else (B,), dev), qp, qop, kp, kop)
+    if q_out is None:
+        q_out = q
+    qp, qs = q.data_ptr(), q.stride()
+    qop, qos = _rope_rows(q_out, "q_out", dtype, shape, dev), q_out.stride()
+    if qp == qop and qs != qos:
+        raise ValueError("q_out: in place needs the input's strides")
+    pos_shape = shape[:1] if len(shape) == 3 else (shape[0], shape[2])
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out given without k")
+        d = _rope_desc(dtype, layout, mscale, inverse, inv_freq.shape[0], shape, 0, qs, qos)
+        kp = kop = None
+    else:
+        if not isinstance(k, torch.Tensor) or k.dim() != len(shape) or k.shape[1] == 0:
+            raise ValueError("k: expected a tensor shaped like q but for its heads (one at least)")
+        if k_out is None:
+            k_out = k
+        kshape = (shape[0], k.shape[1]) + tuple(shape[2:])
+        kp, ks = _rope_rows(k, "k", dtype, kshape, dev), k.stride()
+        kop, kos = _rope_rows(k_out, "k_out", dtype, kshape, dev), k_out.stride()
+        if kp == kop and ks != kos:
+            raise ValueError("k_out: in place needs the input's strides")
+        d = _rope_desc(dtype, layout, mscale, inverse, inv_freq.shape[0], shape, kshape[1], qs, qos, ks, kos)
+    _call("rswa_rope_1d", dev, stream, d, inv_freq.data_ptr(), _tensor(pos, "pos", torch.int32, pos_shape, dev), qp,
+          qop, kp, kop)
     return q_out, k_out
 
 

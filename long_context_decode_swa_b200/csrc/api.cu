@@ -86,9 +86,15 @@ thread_local uint64_t g_test_wait_ns = 0;
 
 namespace rswa {
 int device_sm_count() {
+  static int cached[64] = {};  // by device: the launches ask each time
   int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms > 0 ? sms : 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return sms;
+  const bool slot = dev >= 0 && dev < 64;
+  const int known = slot ? __atomic_load_n(&cached[dev], __ATOMIC_RELAXED) : 0;
+  if (known > 0) return known;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 148;
+  if (slot) __atomic_store_n(&cached[dev], sms, __ATOMIC_RELAXED);
+  return sms;
 }
 }  // namespace rswa
 
@@ -1092,7 +1098,8 @@ rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_freq, const 
     if (!std::isfinite(inv_freq[i])) return fail(RSWA_ERR_INVALID, "%s: inv_freq[%d] is not finite", fn, i);
     // turns per position modulo 1 in 64-bit fixed point; whole turns do not matter to an integer position
     const long double turns = (long double)inv_freq[i] * 0.159154943091895335768883763372514362L;  // 1 / (2 pi)
-    L.turns[i] = (uint64_t)((turns - floorl(turns)) * 18446744073709551616.0L);
+    const long double part = fabsl(turns) < 4611686018427387904.0L ? turns - (long double)(int64_t)turns : 0.0L;
+    L.turns[i] = (uint64_t)(int64_t)(part * 9223372036854775808.0L) << 1;  // |part| < 1, signed
   }
   cudaError_t e = rswa::launch_rope1d(L, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);

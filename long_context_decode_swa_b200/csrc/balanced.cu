@@ -32,6 +32,8 @@ constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileBytes = kBlock * kRowBytes;  // 8 KiB
 constexpr int kCtasPerSm = 2;                   // by shared memory
+constexpr int kSoloItems = 4;
+constexpr int kWholeRounds = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -41,8 +43,9 @@ struct BalancedSmem {
   float wm[kWarps], wl[kWarps], wlu[kWarps];
   float wacc[kWarps][kHeadDim];
   long long scan[kWarps];
-  long long start_base;  // units before the sequence that the CTA's share starts in
-  int start_b;
+  int most[kWarps];
+  long long start_base[kWarps];  // units before the sequence that the team's share starts in
+  int start_b[kWarps];
   int is_last;
 };
 
@@ -100,8 +103,15 @@ __device__ __forceinline__ SeqRows rows_of(const BalancedArgs& a, int b, bool re
   return s;
 }
 
-// One warp's place in the CTA's share: units [first, first + s.tiles) of the share (first may be
-// negative: the share starts inside) belong to (b, h).
+// A team's share of the line: a CTA's, or with `solo` a warp's. Units [0, units) of it; with `whole` it
+// is the items (the (sequence, head)s) that start there, to their ends.
+struct Share {
+  int units;
+  bool whole, solo;
+};
+
+// One warp's place in its share: units [first, first + s.tiles) (first may be negative: the share
+// starts inside) belong to (b, h).
 struct Cursor {
   int b, h;
   int first;
@@ -123,15 +133,16 @@ struct Tile {
   int row0;  // first prefix row (>= 0), or ~ of the first ring slot
 };
 
-// Issues unit u of the share (if u < share) into this warp's stage.
+// Issues unit u of the share (if it has it) into this warp's stage.
 template <bool kScored>
-__device__ __forceinline__ Tile issue(const BalancedArgs& a, BalancedSmem& sm, int u, int share, Cursor& c, int warp,
-                                      int lane) {
+__device__ __forceinline__ Tile issue(const BalancedArgs& a, BalancedSmem& sm, int u, const Share& share, Cursor& c,
+                                      int warp, int lane) {
   Tile t;
   t.rows = 0;
   t.row0 = 0;
-  if (u >= share) return t;
-  while (u >= c.first + c.s.tiles) advance<kScored>(a, c);
+  if (!share.whole && u >= share.units) return t;
+  while (c.first < share.units && u >= c.first + c.s.tiles) advance<kScored>(a, c);
+  if (c.first >= share.units) return t;
   int i = u - c.first;
   const int64_t bh = (int64_t)c.b * a.H + c.h;
   const uint16_t *k, *v;
@@ -285,27 +296,49 @@ __device__ __forceinline__ void join(State& s, const float* rec, int c) {
   s.acc[3] = make_float2(fmaf(s.acc[3].x, fs, r1.z * fr), fmaf(s.acc[3].y, fs, r1.w * fr));
 }
 
-// The records that the shared part left for (b, h): one for each CTA that had a run of its keys.
+// Where the shared part's records of a sequence lie: one a head for each CTA that had a run of its keys.
+struct SharedSeq {
+  int row;  // -1: none
+  int first_seq, rows, key_tiles;
+  long long first_unit, per;
+};
+
+__device__ __forceinline__ SharedSeq shared_seq(const BalancedArgs& a, int b) {
+  SharedSeq r;
+  r.row = -1;
+  r.first_seq = r.rows = r.key_tiles = 0;
+  r.first_unit = r.per = 1;
+  const int ti = a.shared.seq_tile[b];
+  if (ti < 0) return r;
+  const SharedTile t = a.shared.tiles[ti];
+  r.row = a.shared.seq_row[b];
+  r.first_seq = t.first_seq;
+  r.rows = t.rows;
+  r.key_tiles = t.key_tiles;
+  r.first_unit = t.first_unit;
+  r.per = a.shared.head->per;
+  return r;
+}
+
 struct SharedRecords {
   int count;
   const float* first;  // the run that holds the first key tile
   const float* next;   // the others, kSharedRows records apart
+  __device__ __forceinline__ const float* at(int r) const {
+    return r == 0 ? first : next + (int64_t)(r - 1) * kSharedRows * kRecordFloats;
+  }
 };
 
-__device__ __forceinline__ SharedRecords shared_records(const BalancedArgs& a, int b, int h) {
+__device__ __forceinline__ SharedRecords shared_records(const BalancedArgs& a, const SharedSeq& t, int h) {
   SharedRecords r;
   r.count = 0;
   r.first = r.next = nullptr;
-  const int ti = a.shared.seq_tile[b];
-  if (ti < 0) return r;
-  const int row = a.shared.seq_row[b];
-  const SharedTile t = a.shared.tiles[ti];
-  const long long per = a.shared.head->per;
+  if (t.row < 0) return r;
   const long long u = t.first_unit + (long long)h * t.key_tiles;
-  const int c0 = (int)(u / per), c1 = (int)((u + t.key_tiles - 1) / per);
+  const int c0 = (int)(u / t.per), c1 = (int)((u + t.key_tiles - 1) / t.per);
   r.count = c1 - c0 + 1;
-  r.first = a.shared.records + ((int64_t)t.first_seq * a.H + (int64_t)h * t.rows + row) * kRecordFloats;
-  r.next = a.shared.records + ((int64_t)a.B * a.H + (int64_t)(c0 + 1) * kSharedRows + row) * kRecordFloats;
+  r.first = a.shared.records + ((int64_t)t.first_seq * a.H + (int64_t)h * t.rows + t.row) * kRecordFloats;
+  r.next = a.shared.records + ((int64_t)a.B * a.H + (int64_t)(c0 + 1) * kSharedRows + t.row) * kRecordFloats;
   return r;
 }
 
@@ -326,55 +359,91 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
   const int per_thread = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per_thread), b1 = min(a.B, b0 + per_thread);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += rows_of<kScored>(a, b, blockIdx.x == 0).tiles;
+  int most = 0;  // tiles of the longest item
+  for (int b = b0; b < b1; ++b) {
+    const int tiles = rows_of<kScored>(a, b, blockIdx.x == 0).tiles;
+    mine += tiles;
+    most = max(most, tiles);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long t = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += t;
   }
-  if (lane == 31) sm.scan[warp] = inc;
+  if (lane == 31) {
+    sm.scan[warp] = inc;
+    sm.most[warp] = most;
+  }
   __syncthreads();
   long long before = inc - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     before += w < warp ? sm.scan[w] : 0;
     total += sm.scan[w];
+    most = max(most, sm.most[w]);
   }
   before *= a.H;
   mine *= a.H;
   total *= a.H;
+  // How the line is cut. Items that are short against a share go whole: to a warp each where every
+  // warp gets at least kSoloItems of them (no barrier at an item's end, next to no imbalance), to a CTA
+  // where a CTA gets that many, and, where there are no more items than CTAs, one to a CTA as long
+  // as it is done in a few rounds of the six warps (records to join cost more). Else shares cut
+  // through items.
   long long per = (total + gridDim.x - 1) / gridDim.x;
-  per = per < a.min_share ? a.min_share : per;
-  const long long u0 = (long long)blockIdx.x * per;
-  if (u0 >= total) return;  // uniform: the whole CTA
-  const int share = (int)min(per, total - u0);
-  if (mine > 0 && u0 >= before && u0 < before + mine) {
-    long long base = before;
-    int b = b0;
-    for (;; ++b) {
-      const long long units = (long long)rows_of<kScored>(a, b, false).tiles * a.H;
-      if (u0 < base + units) break;
-      base += units;
+  Share share;
+  share.solo = per >= (long long)kSoloItems * kWarps * most;
+  share.whole = share.solo || per >= (long long)kSoloItems * most || (per <= most && most <= kWholeRounds * kWarps);
+  if (share.solo)
+    per = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);
+  else
+    per = max(per, (long long)(share.whole ? most : kWarps));  // fewer units than warps: idle warps, more records
+  const int step = share.solo ? 1 : kWarps;
+  const int slot = share.solo ? warp : 0;  // this warp's team in the CTA
+  const long long team0 = (long long)blockIdx.x * (share.solo ? kWarps : 1);
+  for (int w = 0; w < (share.solo ? kWarps : 1); ++w) {
+    const long long u = (team0 + w) * per;
+    if (mine > 0 && u >= before && u < before + mine) {
+      long long base = before;
+      int b = b0;
+      for (;; ++b) {
+        const long long units = (long long)rows_of<kScored>(a, b, false).tiles * a.H;
+        if (u < base + units) break;
+        base += units;
+      }
+      sm.start_b[w] = b;
+      sm.start_base[w] = base;
     }
-    sm.start_b = b;
-    sm.start_base = base;
   }
   __syncthreads();
+  const long long u0 = (team0 + slot) * per;
+  if (u0 >= total) return;  // a whole team: no barrier follows for it
+  share.units = (int)min(per, total - u0);
 
   Cursor ahead;  // where this warp issues copies
-  ahead.b = sm.start_b;
+  ahead.b = sm.start_b[slot];
   ahead.s = rows_of<kScored>(a, ahead.b, false);
-  ahead.h = (int)((u0 - sm.start_base) / ahead.s.tiles);
-  ahead.first = (int)(sm.start_base + (long long)ahead.h * ahead.s.tiles - u0);
+  ahead.h = (int)((u0 - sm.start_base[slot]) / ahead.s.tiles);
+  ahead.first = (int)(sm.start_base[slot] + (long long)ahead.h * ahead.s.tiles - u0);
+  if (share.whole && ahead.first < 0) {  // that item is another team's
+    if (u0 + ahead.first + ahead.s.tiles >= total) return;
+    advance<kScored>(a, ahead);
+    if (ahead.first >= share.units) return;
+  }
   Cursor at = ahead;  // the (sequence, head) being read
-  Tile tile = issue<kScored>(a, sm, warp, share, ahead, warp, lane);
+  int u = at.first > 0 ? at.first : 0;  // with `whole`, units before its first item are another team's
+  u += share.solo ? 0 : warp;
+  Tile tile = issue<kScored>(a, sm, u, share, ahead, warp, lane);
+  SharedSeq seq;
+  int seq_b = -1;
+  uint4 q_next = *reinterpret_cast<const uint4*>(a.q + ((int64_t)at.b * a.H + at.h) * kHeadDim + c * 8);
   uint32_t phase = 0;
   bool ok = true;
-  int u = warp;
 
   while (true) {
-    const int end = min(share, at.first + at.s.tiles);
+    const int end = share.whole ? at.first + at.s.tiles : min(share.units, at.first + at.s.tiles);
     const int64_t bh = (int64_t)at.b * a.H + at.h;
     Score sc;
     sc.cap_log2 = sc.slope_log2 = 0.f;
@@ -403,14 +472,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
     }
     float2 q2[4];
     {
-      const uint4 qw = *reinterpret_cast<const uint4*>(a.q + bh * kHeadDim + c * 8);
-      const uint32_t ws[4] = {qw.x, qw.y, qw.z, qw.w};
+      const uint32_t ws[4] = {q_next.x, q_next.y, q_next.z, q_next.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) q2[e] = make_float2(bf16lo(ws[e]) * qmul, bf16hi(ws[e]) * qmul);
     }
+    if (bh + 1 < (int64_t)a.B * a.H)  // the next item's query, while this one streams
+      q_next = *reinterpret_cast<const uint4*>(a.q + (bh + 1) * kHeadDim + c * 8);
+    SharedRecords sr;
+    sr.count = 0;
+    if (kShared) {
+      if (seq_b != at.b) {
+        seq = shared_seq(a, at.b);
+        seq_b = at.b;
+      }
+      sr = shared_records(a, seq, at.h);
+    }
     State st;
     clear(st);
-    for (; ok && u < end; u += kWarps) {
+    for (; ok && u < end; u += step) {
       const Tile cur = tile;
       if (cur.rows > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp], phase))) {
@@ -425,17 +504,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
           consume<kScored, false>(sm.stage[warp][0], sm.stage[warp][1], cur, sc, q2, g, c, st);
       }
       __syncwarp();  // every lane has read the stage before it is filled again
-      tile = issue<kScored>(a, sm, u + kWarps, share, ahead, warp, lane);
+      tile = issue<kScored>(a, sm, u + step, share, ahead, warp, lane);
     }
     fold(st);
-    const bool starts = at.first >= 0, ends = at.first + at.s.tiles <= share;
-    SharedRecords sr;
-    sr.count = 0;
-    if (kShared) {
-      sr = shared_records(a, at.b, at.h);
-      if (starts && ends)  // the whole item is here: the shared part's records join its warps
-        for (int r = warp; r < sr.count; r += kWarps)
-          join(st, r == 0 ? sr.first : sr.next + (int64_t)(r - 1) * kSharedRows * kRecordFloats, c);
+    const bool starts = at.first >= 0, ends = share.whole || at.first + at.s.tiles <= share.units;
+    if (kShared && starts && ends)  // the whole item is here: the shared part's records join its warps
+      for (int r = share.solo ? 0 : warp; r < sr.count; r += step) join(st, sr.at(r), c);
+
+    if (share.solo) {
+      if (g == 0 && ok) {
+        const float inv = st.l == 0.f ? 0.f : 1.f / st.l;  // no row seen: zero (a NaN sum stays one)
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] = st.acc[e].x * inv;
+          o[2 * e + 1] = st.acc[e].y * inv;
+        }
+        if (kShared) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 o2 = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&o2);
+          }
+          reinterpret_cast<uint4*>(a.out)[bh * (kHeadDim / 8) + c] = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          float4* out = reinterpret_cast<float4*>(a.out) + bh * (kHeadDim / 4) + 2 * c;
+          out[0] = make_float4(o[0], o[1], o[2], o[3]);
+          out[1] = make_float4(o[4], o[5], o[6], o[7]);
+        }
+        if (c == 0 && a.lse)
+          a.lse[bh] = st.lu == 0.f ? -INFINITY : (st.m + log2f(st.lu) - sc.slope_log2 * (float)sc.ref) * kLn2;
+      }
+      if (!ok || end >= share.units) break;
+      advance<kScored>(a, at);
+      continue;
     }
 
     // ---- the warps' states meet; `joined` says that st holds records of the whole item ----
@@ -500,19 +603,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
       clear(st);
       for (int r = warp; r <= c1 - c0 + sr.count; r += kWarps) {
         const int k = r - (c1 - c0 + 1);
-        join(st, k < 0 ? a.records + (int64_t)(2 * (c0 + r) + (r == 0 ? 1 : 0)) * kRecordFloats
-                       : (k == 0 ? sr.first : sr.next + (int64_t)(k - 1) * kSharedRows * kRecordFloats), c);
+        join(st, k < 0 ? a.records + (int64_t)(2 * (c0 + r) + (r == 0 ? 1 : 0)) * kRecordFloats : sr.at(k), c);
       }
     }
     // the merge buffers are written again by the next item; a warp that gave up ends the CTA
-    if (__syncthreads_or(!ok) || !ends || end == share) break;
+    if (__syncthreads_or(!ok) || !ends || end >= share.units) break;
     advance<kScored>(a, at);
   }
   // after a give-up the copy issued last may be in flight: let it land (bounded) before the
   // shared memory goes away
-  if (!ok || u < share) {
-    if (tile.rows > 0) mbar_wait(&sm.full[warp], phase);
-  }
+  if (!ok && tile.rows > 0) mbar_wait(&sm.full[warp], phase);
 }
 
 }  // namespace
@@ -529,8 +629,6 @@ cudaError_t launch_balanced(BalancedArgs a, void* scratch, cudaStream_t stream) 
   const int grid = balanced_grid();
   a.counters = static_cast<int32_t*>(scratch);
   a.records = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + ((size_t)grid * 4 + 255) / 256 * 256);
-  // a share of fewer units than warps would trade idle warps for more records to join
-  a.min_share = kWarps;
   const bool shared = a.shared.head != nullptr;
   auto kernel = shared ? balanced_kernel<false, true> : balanced_kernel<true, false>;
   cudaError_t e = ensure_smem_limit(kernel, sizeof(BalancedSmem), &done[shared ? 1 : 0]);

@@ -64,7 +64,6 @@ struct BalancedArgs {
   // set by launch_balanced
   int32_t* counters;
   float* records;
-  int min_share;
 };
 
 int balanced_grid();

@@ -8,8 +8,7 @@
 // key tile of 128 rows, some 2,700 cycles of one SM's share of HBM, against 512 cycles of MMA
 // and about 1,000 of exponentials); above that the exponentials.
 //
-// group_kernel (one CTA): sorts the sequences by prefix, stably, so that a call's cut and with it
-// its rounding depend on the inputs alone, and lays the tables out. shared_kernel: one CTA an SM;
+// group_kernel (one CTA): sorts the sequences by prefix and lays the tables out. shared_kernel: one CTA an SM;
 // the work is a line of units (a key tile of one head of one tile of sequences) cut evenly over the
 // CTAs, so few long prefixes fill the chip as well as many short ones. A CTA walks its run in
 // segments, one per (tile, head), with roles as in the chunked prefill:
@@ -64,42 +63,58 @@ struct GroupArgs {
   int32_t* status;
 };
 
-// Exclusive scan of v over the block; total over all threads.
-template <typename V>
-__device__ V block_scan(V v, V* warps, V& total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  V inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const V t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
-  }
-  __syncthreads();
-  if (lane == 31) warps[warp] = inc;
-  __syncthreads();
-  V before = 0;
-  total = 0;
-  for (int w = 0; w < kGroupThreads / 32; ++w) {
-    const V x = warps[w];
-    before += w < warp ? x : 0;
-    total += x;
-  }
-  return before + inc - v;
+struct Counts {
+  long long seqs, tiles, units;
+};
+
+__device__ __forceinline__ Counts plus(const Counts& a, const Counts& b) {
+  return Counts{a.seqs + b.seqs, a.tiles + b.tiles, a.units + b.units};
 }
 
+__device__ __forceinline__ Counts warp_scan(Counts v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Counts t = Counts{__shfl_up_sync(0xffffffffu, v.seqs, o), __shfl_up_sync(0xffffffffu, v.tiles, o),
+                            __shfl_up_sync(0xffffffffu, v.units, o)};
+    if (lane >= o) v = plus(v, t);
+  }
+  return v;
+}
+
+// Exclusive scan of v over the block (warps: 32 entries of shared memory); total over all threads.
+__device__ Counts block_scan(const Counts& v, Counts* warps, Counts& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
+  const Counts inc = warp_scan(v, lane);
+  if (lane == 31) warps[warp] = inc;
+  __syncthreads();
+  const Counts sums = warp_scan(lane < n ? warps[lane] : Counts{0, 0, 0}, lane);
+  total = Counts{__shfl_sync(0xffffffffu, sums.seqs, 31), __shfl_sync(0xffffffffu, sums.tiles, 31),
+                 __shfl_sync(0xffffffffu, sums.units, 31)};
+  const int from = warp > 0 ? warp - 1 : 0;
+  Counts before = Counts{__shfl_sync(0xffffffffu, sums.seqs, from), __shfl_sync(0xffffffffu, sums.tiles, from),
+                         __shfl_sync(0xffffffffu, sums.units, from)};
+  if (warp == 0) before = Counts{0, 0, 0};
+  __syncthreads();  // warps[] is written again
+  return plus(before, Counts{inc.seqs - v.seqs, inc.tiles - v.tiles, inc.units - v.units});
+}
+
+// blockDim.x: a multiple of 32, at most 1,024.
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a) {
   extern __shared__ int tab[];
-  int* count = tab;           // sequences of prefix p
-  int* first = tab + a.P;     // its first place in order[]
+  int* count = tab;            // sequences of prefix p
+  int* first = tab + a.P;      // its first place in order[]
   int* tile0 = tab + 2 * a.P;  // its first tile (-1: no rows, or nobody reads it)
-  __shared__ long long scan[kGroupThreads / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ Counts scan[kGroupThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
+  for (int p = tid; p < a.P; p += threads) count[p] = 0;
   griddep_wait();
   griddep_launch_dependents();
-  for (int p = tid; p < a.P; p += kGroupThreads) count[p] = 0;
   __syncthreads();
-  // each sequence's rank among its prefix's, in order of the sequences
-  for (int base = 0; base < a.B; base += kGroupThreads) {
+  // Each sequence's rank among its prefix's. A row's arithmetic does not depend on its place in a
+  // tile, so any order will do while a prefix's sequences fit one tile; where they do not, ranks go by the
+  // sequences' order, so that their cut, and with it the rounding, is the same in every call.
+  bool more = false;
+  for (int base = 0; base < a.B; base += threads) {
     const int b = base + tid;
     int p = b < a.B ? a.share_of[b] : -1;
     if (p < -1 || p >= a.P) {
@@ -109,22 +124,36 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a)
     const unsigned same = __match_any_sync(0xffffffffu, p);
     const int leader = __ffs(same) - 1;
     int rank = 0;
-    const int warps = min(kGroupThreads / 32, (a.B - base + 31) / 32);
-    for (int w = 0; w < warps; ++w) {
-      if (warp == w && lane == leader && p >= 0) {
-        rank = count[p];
-        count[p] = rank + __popc(same);
-      }
-      __syncthreads();
-    }
+    if (lane == leader && p >= 0) rank = atomicAdd(&count[p], __popc(same));
     rank = __shfl_sync(0xffffffffu, rank, leader) + __popc(same & ((1u << lane) - 1));
+    more |= p >= 0 && rank >= kSharedRows;
     if (b < a.B) {
       a.seq_tile[b] = p;
       a.seq_row[b] = rank;
     }
   }
-  long long seqs = 0, tiles = 0, units = 0;  // so far
-  for (int base = 0; base < a.P; base += kGroupThreads) {
+  if (__syncthreads_or(more)) {
+    for (int p = tid; p < a.P; p += threads) count[p] = 0;
+    __syncthreads();
+    for (int base = 0; base < a.B; base += threads) {
+      const int b = base + tid;
+      const int p = b < a.B ? a.seq_tile[b] : -1;
+      const unsigned same = __match_any_sync(0xffffffffu, p);
+      const int leader = __ffs(same) - 1;
+      int rank = 0;
+      for (int w = 0; w < threads / 32; ++w) {
+        if (warp == w && lane == leader && p >= 0) {
+          rank = count[p];
+          count[p] = rank + __popc(same);
+        }
+        __syncthreads();
+      }
+      rank = __shfl_sync(0xffffffffu, rank, leader) + __popc(same & ((1u << lane) - 1));
+      if (b < a.B) a.seq_row[b] = rank;
+    }
+  }
+  Counts sum{0, 0, 0};  // so far
+  for (int base = 0; base < a.P; base += threads) {
     const int p = base + tid;
     int n = p < a.P ? count[p] : 0;
     int len = 0;
@@ -139,41 +168,37 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a)
     const int nt = (n + kSharedRows - 1) / kSharedRows;
     const int keys = (len + kRows - 1) / kRows;
     const long long each = (long long)keys * a.H;
-    long long t_seqs, t_tiles, t_units;
-    const long long s0 = seqs + block_scan<long long>(n, scan, t_seqs);
-    const long long k0 = tiles + block_scan<long long>(nt, scan, t_tiles);
-    const long long u0 = units + block_scan<long long>(nt * each, scan, t_units);
+    Counts total;
+    const Counts at = plus(sum, block_scan(Counts{n, nt, nt * each}, scan, total));
     if (p < a.P) {
-      first[p] = (int)s0;
-      tile0[p] = nt > 0 ? (int)k0 : -1;
+      first[p] = (int)at.seqs;
+      tile0[p] = nt > 0 ? (int)at.tiles : -1;
       for (int i = 0; i < nt; ++i) {
         SharedTile t;
-        t.first_unit = u0 + i * each;
-        t.first_seq = (int)s0 + i * kSharedRows;
+        t.first_unit = at.units + i * each;
+        t.first_seq = (int)at.seqs + i * kSharedRows;
         t.rows = min(kSharedRows, n - i * kSharedRows);
         t.prefix = p;
         t.len = len;
         t.key_tiles = keys;
         t.pad = 0;
-        a.tiles[k0 + i] = t;
+        a.tiles[at.tiles + i] = t;
       }
     }
-    seqs += t_seqs;
-    tiles += t_tiles;
-    units += t_units;
+    sum = plus(sum, total);
+  }
+  if (tid == 0) {
+    a.head->units = sum.units;
+    a.head->per = max(1ll, (sum.units + a.ctas - 1) / a.ctas);
+    a.head->tiles = (int)sum.tiles;
   }
   __syncthreads();
-  for (int b = tid; b < a.B; b += kGroupThreads) {  // the rows this thread wrote above
+  for (int b = tid; b < a.B; b += threads) {  // the rows this thread wrote above
     const int p = a.seq_tile[b], rank = a.seq_row[b];
     const bool has = p >= 0 && tile0[p] >= 0;
     if (has) a.order[first[p] + rank] = b;
     a.seq_tile[b] = has ? tile0[p] + rank / kSharedRows : -1;
     a.seq_row[b] = rank % kSharedRows;
-  }
-  if (tid == 0) {
-    a.head->units = units;
-    a.head->per = max(1ll, (units + a.ctas - 1) / a.ctas);
-    a.head->tiles = (int)tiles;
   }
 }
 
@@ -665,7 +690,8 @@ cudaError_t launch_shared(const SharedLaunch& L, void* scratch, SharedTables* ta
   if ((e = ensure_smem_limit(group_kernel, (size_t)kMaxShared * 12, &done[0])) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  fill_launch_config(cfg, attr, dim3(1), dim3(kGroupThreads), tab, stream);
+  const int want = ((L.B > L.P ? L.B : L.P) + 31) / 32 * 32;
+  fill_launch_config(cfg, attr, dim3(1), dim3(want < kGroupThreads ? want : kGroupThreads), tab, stream);
   if ((e = cudaLaunchKernelEx(&cfg, group_kernel, g)) != cudaSuccess) return e;
 
   tables->head = g.head;

@@ -5,19 +5,25 @@
 // i - n < j <= i and, for j < 0, to the previous chunk's last outputs in the ring, with
 //   s = cap tanh(scale q.k / cap) - slope_h (pos_q - pos_k).
 //
-// A CTA owns two 128-row query tiles (A and B) of one (sequence, head) and walks the key tiles (128
-// keys) that any of its rows sees; the roles are those of the plain prefill (prefill.cu): TMA
-// producers in warps 0 (Q, K) and 2 (V), the MMA issuer in warp 1, softmax of tile A in warps 4-7
-// and of tile B in warps 8-11, thread r owning row r; P (bf16) replaces S in TMEM and is the A
-// operand of P V.
+// A CTA has two streams of work, A and B, each a 128-row query tile against key tiles of 128 rows:
+//   paired (many queries): A and B are neighbouring query tiles and walk the same key tiles, so a
+//     key tile is fetched once for 256 queries;
+//   split (few queries): A and B are the same query tile and take every other key tile, and a
+//     cluster of up to 8 CTAs deals the key tiles out among its CTAs; the parts meet through shared
+//     memory, the CTAs' through distributed shared memory.
+// While one stream's softmax runs, the tensor core works on the other's products. Roles: warp 0 TMA
+// producer of Q and K, warp 2 of V, warp 1 MMA issuer, warps 4-7 / 8-11 softmax of stream A / B, thread r
+// owning row r: its 128 scores are read from TMEM once and stay in registers (the softmax warps take
+// the registers that the others give up), and P (bf16) goes back over S as the A operand of P V.
 //
-// Documents: the union of the 256 rows' ranges, as up to four runs of rows, gives the prefix tiles;
-// rows of a tile that none of them sees are zeroed in V (0 * NaN would reach O). A chunk over packed
-// documents so costs what its documents cost, not what the prefix does.
+// Documents: the union of the rows' ranges, as up to four runs of rows, gives the prefix tiles;
+// rows of a tile that no query of the CTA sees are zeroed in V (0 * NaN would reach O). A chunk over
+// packed documents so costs what its documents cost, not what the prefix does.
 //
-// Scores: tanh(u) = 1 - 2 / (e^2u + 1), by one ex2 and one rcp of the special-function unit (16 a
-// cycle and SM); with the softmax's own ex2 that is three a score, 3,072 cycles a tile against 512
-// of MMA. The cancellation at small u costs 2^-23 of the cap, not of the score: 1e-5 at cap 50.
+// Scores: the special-function unit (16 a cycle and SM) bounds the kernel: one ex2 a score is 1,024
+// cycles a tile against 512 of MMA. tanh(u) = 1 - 2 / (e^2u + 1) would cost two more; where a warp's
+// scores all have |u| = |scale q.k| / cap <= 0.6 (or 1), tanh is u times a minimax polynomial in u^2
+// instead, on the packed FMA pipe (errors below 1e-7 of the cap either way).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -34,14 +40,20 @@ namespace rswa {
 namespace {
 
 constexpr int kRows = 128;                 // query rows per tile, keys per key tile
-constexpr int kQTiles = 2;                 // query tiles per CTA
-constexpr int kCtaRows = kQTiles * kRows;
+constexpr int kQTiles = 2;                 // query tiles of a paired CTA, streams of any
+constexpr int kMaxRows = kQTiles * kRows;
 constexpr int kRegionBytes = kRows * 128;  // one 64-column SW128 region of a 128-row tile
 constexpr int kTileBytes = 2 * kRegionBytes;
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4;
+constexpr int kMaxCluster = 8;
+// Registers a thread after the split: the block is launched with kLaunchRegs each (checked by
+// launch_scored_prefill), and the two shares must fit that.
+constexpr int kLaunchRegs = 168, kControlRegs = 80, kSoftmaxRegs = 208;
+static_assert(128 * kControlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kPartStride = kHeadDim + 4;  // floats of a row's part in shared memory (keeps rows off one bank)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr float kLazyRescaleLog2 = 8.f;
@@ -70,9 +82,11 @@ struct __align__(1024) Smem {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  int skip;
   Ctx ctx;
+  float stat_m[2][kRows];  // split: the streams' maxima,
+  float stat_l[2][kRows];  // and sums; [0] then holds the CTA's
 };
+static_assert((kKStages + kVStages) * kTileBytes >= kRows * kPartStride * 4, "parts lie over the K / V stages");
 
 struct Args {
   int B, H, n, T;
@@ -85,6 +99,7 @@ struct Args {
   const float* slopes;    // [H], with pos [B], or null
   const int32_t* pos;
   float softcap, scale;
+  int cluster;            // split: CTAs that share a query tile's key tiles
   __nv_bfloat16* out;
   float* lse;
   int32_t* status;
@@ -127,12 +142,6 @@ __device__ __forceinline__ bool tile_visible(const Ctx& c, int X, int kind, int 
   return start <= ihi && jhi >= ilo - c.n + 1;
 }
 
-__device__ __forceinline__ bool tile_visible(const Ctx& c, int X, int t) {
-  int kind, start;
-  tile_kind(c, t, kind, start);
-  return tile_visible(c, X, kind, start);
-}
-
 // The prefix rows query i of sequence b sees (empty: 0, 0).
 __device__ __forceinline__ int2 range_of(const Args& a, int m, int b, int i, bool report) {
   if (i >= a.T) return make_int2(0, 0);
@@ -154,64 +163,209 @@ __device__ __forceinline__ bool wait_or_abort(Smem& sm, uint64_t* bar, uint32_t 
   return false;
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// What a row does to its raw scores. In the log2 domain: s = mul raw (no cap), or
-// cap2 - 2 cap2 / (2^(mul raw) + 1), plus slope2 (column - away0).
-struct RowScore {
-  float mul, cap2, slope2;
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+
+// u -> cap2 tanh(u), u = raw k, for pairs: minimax polynomials (error 2e-8 of tanh on their range).
+template <int kTerms>
+__device__ __forceinline__ float2 tanh_poly(float2 raw, float k, const float (&coef)[kTerms], float cap2) {
+  const float2 u = __fmul2_rn(raw, splat(k));
+  const float2 w = __fmul2_rn(u, u);
+  float2 p = splat(coef[kTerms - 1] * cap2);
+#pragma unroll
+  for (int i = kTerms - 2; i >= 0; --i) p = __ffma2_rn(p, w, splat(coef[i] * cap2));
+  return __fmul2_rn(u, p);
+}
+
+constexpr float kTanhSmall = 0.6f, kTanhMid = 1.f;
+
+// Visible columns [lo, hi) of a tile as bits of its w-th 32 columns.
+__device__ __forceinline__ uint32_t column_bits(int lo, int hi, int w) {
+  const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
+  const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1, below_a = a == 32 ? 0xffffffffu : (1u << a) - 1;
+  return below_b & ~below_a;
+}
+
+// A row's view of one key tile: columns [lo, hi) and [lo2, hi2) are visible; column e is at distance
+// base - e (less the row's reference distance), and n further on from column cut (the ring's wrap).
+struct RowTile {
+  int lo, hi, lo2, hi2;
+  int base, cut;
 };
 
-template <bool kCap>
-__device__ __forceinline__ float scored(const RowScore& s, float raw) {
-  if (!kCap) return raw * s.mul;
-  return fmaf(-2.f * s.cap2, rcp(ex2(raw * s.mul) + 1.f), s.cap2);
-}
-
-// The scores of one 32-column chunk: masked columns -inf. fbase: the distance of the tile's column 0
-// (less the row's reference distance).
-template <bool kCap, bool kBias>
-__device__ __forceinline__ void score_chunk(const Ctx& c, const RowScore& rs, int kind, int start, int col0, int lo, int hi,
-                                            int i, int base, bool full, const uint32_t (&r)[32], float (&x)[32]) {
-  if (kind == kRing) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int slot = start + col0 + e, age = ring_age(c, slot);
-      float s = scored<kCap>(rs, __uint_as_float(r[e]));
-      if (kBias) s = fmaf(-rs.slope2, (float)(base + age), s);
-      x[e] = (slot < c.n && age <= c.fill && age < c.n - i) ? s : -INFINITY;
+__device__ __forceinline__ RowTile row_tile(const Ctx& c, int kind, int start, int i, const int2& range, int pos, int ref) {
+  RowTile t;
+  t.lo2 = t.hi2 = 0;
+  t.cut = kRows;
+  if (kind == kPrefix) {
+    t.lo = range.x - start;
+    t.hi = range.y - start;
+    t.base = pos - start - ref;
+  } else if (kind == kBand) {
+    t.lo = i - c.n + 1 - start;
+    t.hi = min(i, c.T - 1) + 1 - start;
+    t.base = i - start - ref;
+  } else {
+    // slots of ages 1 .. left: wp - 1 down to wp - left, round the ring's end
+    const int left = min(c.fill, c.n - 1 - i);
+    t.lo = max(c.wp - left, 0) - start;
+    t.hi = (left > 0 ? c.wp : 0) - start;
+    if (left > c.wp) {
+      t.lo2 = c.n + c.wp - left - start;
+      t.hi2 = c.n - start;
     }
-    return;
+    t.base = i + c.wp - start - ref;
+    t.cut = c.wp - start;
   }
-  const float b0 = kBias ? rs.slope2 * (float)(col0 - base) : 0.f;
+  return t;
+}
+
+// Raw scores -> scores in the log2 domain, masked ones -inf. k: scale / cap, or scale log2(e) without a
+// cap; full (uniform over the warp): nothing is masked.
+template <bool kCap, bool kBias>
+__device__ __forceinline__ void score_row(float (&x)[kRows], const RowTile& t, bool full, float k, float cap2, float slope2,
+                                          int n) {
+  if (kCap) {
+    float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    float s = scored<kCap>(rs, __uint_as_float(r[e]));
-    if (kBias) s += fmaf(rs.slope2, (float)e, b0);
-    x[e] = (full || (col0 + e >= lo && col0 + e < hi)) ? s : -INFINITY;
+    for (int e = 0; e < kRows; e += 4) {
+      a0 = max3(a0, fabsf(x[e]), fabsf(x[e + 1]));
+      a1 = max3(a1, fabsf(x[e + 2]), fabsf(x[e + 3]));
+    }
+    const float u = fmaxf(a0, a1) * k;
+    if (__all_sync(0xffffffffu, u <= kTanhSmall)) {
+      const float coef[5] = {0.999999627f, -0.333312086f, 0.132992102f, -0.0516967431f, 0.0149769602f};
+#pragma unroll
+      for (int e = 0; e < kRows; e += 2) {
+        const float2 s2 = tanh_poly(make_float2(x[e], x[e + 1]), k, coef, cap2);
+        x[e] = s2.x;
+        x[e + 1] = s2.y;
+      }
+    } else if (__all_sync(0xffffffffu, u <= kTanhMid)) {
+      const float coef[7] = {0.999999693f,  -0.333321293f, 0.133195837f,  -0.0532658353f,
+                             0.0199732827f, -0.00595128048f, 0.000963772187f};
+#pragma unroll
+      for (int e = 0; e < kRows; e += 2) {
+        const float2 s2 = tanh_poly(make_float2(x[e], x[e + 1]), k, coef, cap2);
+        x[e] = s2.x;
+        x[e + 1] = s2.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kRows; ++e) x[e] = fmaf(-2.f * cap2, rcp(ex2(x[e] * (k * 2.f * kLog2e)) + 1.f), cap2);
+    }
+  } else if (kBias) {
+#pragma unroll
+    for (int e = 0; e < kRows; e += 2) {
+      const float2 s2 = __fmul2_rn(make_float2(x[e], x[e + 1]), splat(k));
+      x[e] = s2.x;
+      x[e + 1] = s2.y;
+    }
+  }
+  if (kBias) {
+    // -slope (base - e) = slope e + c0: exact integers, one rounding of the bias
+    const float c0 = -slope2 * (float)t.base;
+    if (t.cut >= kRows) {
+#pragma unroll
+      for (int e = 0; e < kRows; e += 2) {
+        const float2 b2 = __ffma2_rn(splat(slope2), make_float2((float)e, (float)(e + 1)), splat(c0));
+        const float2 s2 = __fadd2_rn(make_float2(x[e], x[e + 1]), b2);
+        x[e] = s2.x;
+        x[e + 1] = s2.y;
+      }
+    } else {
+      const float c1 = -slope2 * (float)(t.base + n);
+#pragma unroll
+      for (int e = 0; e < kRows; ++e) x[e] += fmaf(slope2, (float)e, e < t.cut ? c0 : c1);
+    }
+  }
+  if (!full) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t bits = column_bits(t.lo, t.hi, w) | column_bits(t.lo2, t.hi2, w);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[32 * w + e] = (bits >> e) & 1 ? x[32 * w + e] : -INFINITY;
+    }
   }
 }
 
-template <bool kCap, bool kBias>
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// The address of the same shared-memory place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_smem(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+
+__device__ __forceinline__ float peer_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint4 to_bf16x8(const float* o) {
+  uint32_t w[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const __nv_bfloat162 o2 = __floats2bfloat162_rn(o[2 * u], o[2 * u + 1]);
+    w[u] = *reinterpret_cast<const uint32_t*>(&o2);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Both softmax groups meet.
+__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+
+template <bool kCap, bool kBias, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_prefill_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_ko, const __grid_constant__ CUtensorMap tm_vo,
                           const __grid_constant__ CUtensorMap tm_pk, const __grid_constant__ CUtensorMap tm_pv,
                           const __grid_constant__ CUtensorMap tm_rk, const __grid_constant__ CUtensorMap tm_rv) {
-  extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int qt = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  constexpr int kCtaRows = kSplit ? kRows : kMaxRows;
+  const int cluster = kSplit ? a.cluster : 1;
+  const int rank = kSplit ? (int)cluster_rank() : 0;
+  const int qt = kSplit ? blockIdx.x / cluster : blockIdx.x;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bh = (int64_t)b * a.H + h;
+  if ((smem_addr(smem_raw) & 1023u) != 0) {  // it is, with no other shared memory in the kernel
+    if (tid == 0) set_status(a.status, RSWA_DEVICE_PIPELINE);
+    return;
+  }
   griddep_wait();
   griddep_launch_dependents();
   if (tid == 0) {
-    // a CTA of this launch already gave up on a wait: skip the work (the output is flagged invalid)
-    sm.skip = (*reinterpret_cast<volatile int32_t*>(a.status) & RSWA_DEVICE_WAIT_TIMEOUT) != 0;
     sm.abort_flag = 0;
     mbar_init(&sm.q_full, 1);
     for (int s = 0; s < kKStages; ++s) {
@@ -230,8 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  if (sm.skip) return;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem_base)),
                  "r"(kTmemCols)
@@ -239,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == 0) {
     // ---- the CTA's key tiles ----
-    const bool first = qt == 0 && h == 0 && lane == 0;
+    const bool first = qt == 0 && rank == 0 && h == 0 && lane == 0;
     int m = a.cap > 0 ? a.prefix_len[b] : 0;
     if (m < 0 || m > a.cap) {
       if (first) set_status(a.status, RSWA_DEVICE_BAD_PREFIX_LEN);
@@ -255,16 +407,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i0 = qt * kCtaRows;
     int2 rg[kCtaRows / 32];  // lane's rows: 32 u + lane
 #pragma unroll
-    for (int u = 0; u < kCtaRows / 32; ++u) rg[u] = range_of(a, m, b, i0 + 32 * u + lane, h == 0);
+    for (int u = 0; u < kCtaRows / 32; ++u) rg[u] = range_of(a, m, b, i0 + 32 * u + lane, h == 0 && rank == 0);
     Ctx& c = sm.ctx;
-    for (int x = 0; x < kQTiles; ++x) {
+#pragma unroll
+    for (int x = 0; x < kCtaRows / kRows; ++x) {
       int lo = INT32_MAX, hi = 0;
 #pragma unroll
-      for (int u = 0; u < kCtaRows / 32; ++u)
-        if (u / (kRows / 32) == x && rg[u].y > rg[u].x) {
-          lo = min(lo, rg[u].x);
-          hi = max(hi, rg[u].y);
+      for (int u = 0; u < kRows / 32; ++u) {
+        const int2 g = rg[x * (kRows / 32) + u];
+        if (g.y > g.x) {
+          lo = min(lo, g.x);
+          hi = max(hi, g.y);
         }
+      }
       lo = __reduce_min_sync(0xffffffffu, lo);
       hi = __reduce_max_sync(0xffffffffu, hi);
       if (lane == 0) {
@@ -333,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       c.nr = c.fill > 0 && i0 <= a.n - 2 ? (a.n + kRows - 1) / kRows : 0;
       const int jlo = i0 - a.n + 1;
       c.jt0 = jlo > 0 ? jlo / kRows : 0;
-      c.total = np + c.nr + min(i0 + kCtaRows - 1, a.T - 1) / kRows - c.jt0 + 1;
+      const int all = np + c.nr + min(i0 + kCtaRows - 1, a.T - 1) / kRows - c.jt0 + 1;
+      c.total = kSplit ? (all - rank + cluster - 1) / cluster : all;  // key tiles rank, rank + cluster, ...
     }
   }
   tc_fence_before();
@@ -342,176 +498,207 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Ctx& c = sm.ctx;
   const uint32_t tmem = sm.tmem_base;
   const int total = c.total;
+  // this CTA's t-th key tile, and what stream x does with it
+  auto tile_of = [&](int t, int& kind, int& start) { tile_kind(c, kSplit ? t * cluster + rank : t, kind, start); };
+  auto has = [&](int x, int t) {
+    if (kSplit) return (t & 1) == x;
+    int kind, start;
+    tile_kind(c, t, kind, start);
+    return tile_visible(c, x, kind, start);
+  };
 
-  if (warp == 0 || warp == 2) {
-    // ---------------- producers: Q and K tiles (warp 0), V tiles (warp 2) ----------------
-    if (lane == 0) {
-      const bool is_k = warp == 0;
-      if (is_k) {
-        const int qrow = (int)(bh * a.T) + c.i0;
-        mbar_arrive_expect_tx(&sm.q_full, kQTiles * kTileBytes);
-        for (int x = 0; x < kQTiles; ++x) {
-          tma_load_2d(sm.q[x], &tm_q, 0, qrow + x * kRows, &sm.q_full);
-          tma_load_2d(sm.q[x] + kRegionBytes, &tm_q, 64, qrow + x * kRows, &sm.q_full);
-        }
-      }
-      const int stages = is_k ? kKStages : kVStages;
-      uint64_t* full = is_k ? sm.k_full : sm.v_full;
-      uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
-      int t = 0;
-      for (; t < total; ++t) {
-        const int s = t % stages;
-        if (t >= stages && !wait_or_abort(sm, &empty[s], ((t / stages) - 1) & 1, a.status)) break;
-        int kind, start;
-        tile_kind(c, t, kind, start);
-        const CUtensorMap* map = is_k ? (kind == kPrefix ? &tm_pk : (kind == kRing ? &tm_rk : &tm_ko))
-                                      : (kind == kPrefix ? &tm_pv : (kind == kRing ? &tm_rv : &tm_vo));
-        const int64_t rows = kind == kPrefix ? a.cap : (kind == kRing ? a.n : a.T);
-        const int row = (int)(bh * rows) + start;
-        uint8_t* dst = is_k ? sm.k[s] : sm.v[s];
-        mbar_arrive_expect_tx(&full[s], kTileBytes);
-        tma_load_2d(dst, map, 0, row, &full[s]);
-        tma_load_2d(dst + kRegionBytes, map, 64, row, &full[s]);
-      }
-      if (sm.abort_flag) {  // let the copies in flight land before shared memory is released
-        if (is_k) mbar_wait(&sm.q_full, 0);
-        for (int i = max(0, t - stages); i < t; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer (lane 0) + V-row zeroing (whole warp) ----------------
-    constexpr uint32_t kIdescQK = idesc_bf16_m128_n128(0);
-    constexpr uint32_t kIdescPV = idesc_bf16_m128_n128(1);
-    int n_pv[kQTiles] = {0, 0};
-    bool ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.q_full, 0, a.status));
-    auto issue_s = [&](int x, int t) {  // S_x = Q_x K_t^T
+  if (warp < kSoftmaxWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (warp == 0 || warp == 2) {
+      // ---------------- producers: Q and K tiles (warp 0), V tiles (warp 2) ----------------
       if (lane == 0) {
-        const uint32_t q_addr = smem_addr(sm.q[x]);
-        const uint32_t k_addr = smem_addr(sm.k[t % kKStages]);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (uint32_t)(kk >> 2) * kRegionBytes + (uint32_t)(kk & 3) * 32u;
-          tc_mma_ss(tmem + (uint32_t)x * 128u, smem_desc_sw128(q_addr + off, 16, 1024),
-                    smem_desc_sw128(k_addr + off, 16, 1024), kIdescQK, kk > 0);
+        const bool is_k = warp == 0;
+        if (is_k) {
+          const int qrow = (int)(bh * a.T) + c.i0;
+          mbar_arrive_expect_tx(&sm.q_full, kCtaRows / kRows * kTileBytes);
+          for (int x = 0; x < kCtaRows / kRows; ++x) {
+            tma_load_2d(sm.q[x], &tm_q, 0, qrow + x * kRows, &sm.q_full);
+            tma_load_2d(sm.q[x] + kRegionBytes, &tm_q, 64, qrow + x * kRows, &sm.q_full);
+          }
         }
-        tc_commit(&sm.s_full[x]);
+        const int stages = is_k ? kKStages : kVStages;
+        uint64_t* full = is_k ? sm.k_full : sm.v_full;
+        uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
+        int t = 0;
+        for (; t < total; ++t) {
+          const int s = t % stages;
+          if (t >= stages && !wait_or_abort(sm, &empty[s], ((t / stages) - 1) & 1, a.status)) break;
+          int kind, start;
+          tile_of(t, kind, start);
+          const CUtensorMap* map = is_k ? (kind == kPrefix ? &tm_pk : (kind == kRing ? &tm_rk : &tm_ko))
+                                        : (kind == kPrefix ? &tm_pv : (kind == kRing ? &tm_rv : &tm_vo));
+          const int64_t rows = kind == kPrefix ? a.cap : (kind == kRing ? a.n : a.T);
+          const int row = (int)(bh * rows) + start;
+          uint8_t* dst = is_k ? sm.k[s] : sm.v[s];
+          mbar_arrive_expect_tx(&full[s], kTileBytes);
+          tma_load_2d(dst, map, 0, row, &full[s]);
+          tma_load_2d(dst + kRegionBytes, map, 64, row, &full[s]);
+        }
+        if (sm.abort_flag) {  // let the copies in flight land before shared memory is released
+          if (is_k) mbar_wait(&sm.q_full, 0);
+          for (int i = max(0, t - stages); i < t; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
+        }
       }
-      __syncwarp();
-    };
-    auto wait_k = [&](int t) {
-      const bool w = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.k_full[t % kKStages], (t / kKStages) & 1, a.status));
+    } else if (warp == 1) {
+      // ---------------- MMA issuer (lane 0) + V-row zeroing (whole warp) ----------------
+      constexpr uint32_t kIdescQK = idesc_bf16_m128_n128(0);
+      constexpr uint32_t kIdescPV = idesc_bf16_m128_n128(1);
+      int n_pv[kQTiles] = {0, 0};
+      int k_ready = 0;  // key tiles waited for
+      bool ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.q_full, 0, a.status));
       tc_fence_after();
-      return w;
-    };
-    if (ok) {
-      ok = wait_k(0);
-      if (ok) {
-        for (int x = 0; x < kQTiles; ++x)
-          if (tile_visible(c, x, 0)) issue_s(x, 0);
-        if (lane == 0) tc_commit(&sm.k_empty[0]);
-        __syncwarp();
-      }
-    }
-    for (int t = 0; ok && t < total; ++t) {
-      const int vs = t % kVStages;
-      ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[vs], (t / kVStages) & 1, a.status));
-      if (!ok) break;
-      int kind, start;
-      tile_kind(c, t, kind, start);
-      bool zeroed = false;
-      // a prefix tile inside one run is seen whole
-      bool whole = kind == kBand && start + kRows <= c.T;
-      if (kind == kPrefix)
-        for (int r = 0; r < c.runs; ++r)
-          whole |= start >= c.lo[r] && start + kRows <= c.hi[r] && (c.exact || r < kRuns - 1);
-      if (!whole) {
-        for (int r = lane; r < kRows; r += 32) {
-          const int x = start + r;
-          bool some = false;
-          if (kind == kBand) {
-            some = x < c.T;
-          } else if (kind == kRing) {
-            some = x < c.n && ring_age(c, x) <= c.fill;
-          } else if (c.exact) {
-            for (int u = 0; u < c.runs; ++u) some |= x >= c.lo[u] && x < c.hi[u];
-          } else {
-            for (int i = c.i0; !some && i < min(c.i0 + kCtaRows, c.T); ++i) {
-              const int2 g = range_of(a, c.m, b, i, false);
-              some = x >= g.x && x < g.y;
-            }
-          }
-          if (!some) {
-            uint4* row0 = reinterpret_cast<uint4*>(sm.v[vs] + r * 128);
-            uint4* row1 = reinterpret_cast<uint4*>(sm.v[vs] + kRegionBytes + r * 128);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              row0[e] = make_uint4(0, 0, 0, 0);
-              row1[e] = make_uint4(0, 0, 0, 0);
-            }
-            zeroed = true;
-          }
-        }
-        if (__any_sync(0xffffffffu, zeroed)) fence_async_smem();
-        __syncwarp();
-      }
-      const bool next = t + 1 < total;
-      bool k_next = false;
-      for (int x = 0; ok && x < kQTiles; ++x) {
-        if (tile_visible(c, x, kind, start)) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.p_full[x], n_pv[x] & 1, a.status));
-          if (!ok) break;
+      auto wait_k = [&](int t) {  // key tiles up to t have landed
+        for (; k_ready <= t; ++k_ready) {
+          if (!__all_sync(0xffffffffu,
+                          wait_or_abort(sm, &sm.k_full[k_ready % kKStages], (k_ready / kKStages) & 1, a.status)))
+            return false;
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t v_addr = smem_addr(sm.v[vs]);
-            const uint32_t p_tmem = tmem + (uint32_t)x * 128u;
-            const uint32_t o_tmem = tmem + kColO + (uint32_t)x * 128u;
+        }
+        return true;
+      };
+      auto issue_s = [&](int x, int t) {  // S_x = Q K_t^T
+        if (lane == 0) {
+          const uint32_t q_addr = smem_addr(sm.q[kSplit ? 0 : x]);
+          const uint32_t k_addr = smem_addr(sm.k[t % kKStages]);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_ts(o_tmem, p_tmem + (uint32_t)kk * 8u, smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, kRegionBytes, 1024),
-                        kIdescPV, (n_pv[x] > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(&sm.o_done[x]);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (uint32_t)(kk >> 2) * kRegionBytes + (uint32_t)(kk & 3) * 32u;
+            tc_mma_ss(tmem + (uint32_t)x * 128u, smem_desc_sw128(q_addr + off, 16, 1024),
+                      smem_desc_sw128(k_addr + off, 16, 1024), kIdescQK, kk > 0);
           }
+          tc_commit(&sm.s_full[x]);
+        }
+        __syncwarp();
+      };
+      auto free_k = [&](int t) {
+        if (lane == 0) tc_commit(&sm.k_empty[t % kKStages]);
+        __syncwarp();
+      };
+      constexpr int kAhead = kSplit ? 2 : 1;  // a stream's next key tile
+      if (ok && kSplit) {
+        for (int t = 0; ok && t < min(2, total); ++t)
+          if ((ok = wait_k(t))) {
+            issue_s(t, t);
+            free_k(t);
+          }
+      } else if (ok && (ok = wait_k(0))) {
+        for (int x = 0; x < kQTiles; ++x)
+          if (has(x, 0)) issue_s(x, 0);
+        free_k(0);
+      }
+      for (int t = 0; ok && t < total; ++t) {
+        const int vs = t % kVStages;
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[vs], (t / kVStages) & 1, a.status));
+        if (!ok) break;
+        int kind, start;
+        tile_of(t, kind, start);
+        bool zeroed = false;
+        // a prefix tile inside one run is seen whole
+        bool whole = kind == kBand && start + kRows <= c.T;
+        if (kind == kPrefix)
+          for (int r = 0; r < c.runs; ++r)
+            whole |= start >= c.lo[r] && start + kRows <= c.hi[r] && (c.exact || r < kRuns - 1);
+        if (!whole) {
+          for (int r = lane; r < kRows; r += 32) {
+            const int x = start + r;
+            bool some = false;
+            if (kind == kBand) {
+              some = x < c.T;
+            } else if (kind == kRing) {
+              some = x < c.n && ring_age(c, x) <= c.fill;
+            } else if (c.exact) {
+              for (int u = 0; u < c.runs; ++u) some |= x >= c.lo[u] && x < c.hi[u];
+            } else {
+              for (int i = c.i0; !some && i < min(c.i0 + kCtaRows, c.T); ++i) {
+                const int2 g = range_of(a, c.m, b, i, false);
+                some = x >= g.x && x < g.y;
+              }
+            }
+            if (!some) {
+              uint4* row0 = reinterpret_cast<uint4*>(sm.v[vs] + r * 128);
+              uint4* row1 = reinterpret_cast<uint4*>(sm.v[vs] + kRegionBytes + r * 128);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                row0[e] = make_uint4(0, 0, 0, 0);
+                row1[e] = make_uint4(0, 0, 0, 0);
+              }
+              zeroed = true;
+            }
+          }
+          if (__any_sync(0xffffffffu, zeroed)) fence_async_smem();
           __syncwarp();
-          ++n_pv[x];
         }
-        if (next && tile_visible(c, x, t + 1)) {
-          if (!k_next) {
-            ok = wait_k(t + 1);
+        const bool next = t + kAhead < total;
+        for (int x = 0; ok && x < kQTiles; ++x) {
+          if (has(x, t)) {
+            ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.p_full[x], n_pv[x] & 1, a.status));
             if (!ok) break;
-            k_next = true;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t v_addr = smem_addr(sm.v[vs]);
+              const uint32_t p_tmem = tmem + (uint32_t)x * 128u;
+              const uint32_t o_tmem = tmem + kColO + (uint32_t)x * 128u;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ts(o_tmem, p_tmem + (uint32_t)kk * 8u,
+                          smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, kRegionBytes, 1024), kIdescPV,
+                          (n_pv[x] > 0 || kk > 0) ? 1u : 0u);
+              tc_commit(&sm.o_done[x]);
+            }
+            __syncwarp();
+            ++n_pv[x];
           }
-          issue_s(x, t + 1);
+          if (next && has(x, t + kAhead)) {
+            if (!(ok = wait_k(t + kAhead))) break;
+            issue_s(x, t + kAhead);
+          }
         }
-      }
-      if (!ok) break;
-      if (lane == 0) tc_commit(&sm.v_empty[vs]);
-      if (next) {
-        if (!k_next) {  // no query tile needed it: still let the copy land before freeing the stage
-          ok = wait_k(t + 1);
-          if (!ok) break;
+        if (!ok) break;
+        if (lane == 0) tc_commit(&sm.v_empty[vs]);
+        if (next) {
+          if (!(ok = wait_k(t + kAhead))) break;  // also where no stream needed it: the copy lands before its stage is freed
+          free_k(t + kAhead);
         }
-        if (lane == 0) tc_commit(&sm.k_empty[(t + 1) % kKStages]);
+        __syncwarp();
       }
-      __syncwarp();
+      if (lane == 0) tc_commit(&sm.drain);  // fires once every issued MMA is done
     }
-    if (lane == 0) tc_commit(&sm.drain);  // fires once every issued MMA is done
-  } else if (warp >= kSoftmaxWarp0) {
-    // ---------------- softmax: thread r owns row r of its tile ----------------
+    __syncwarp();
+    if (kSplit && cluster > 1) {
+      cluster_sync();
+      cluster_sync();
+    }
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after();
+      if (lane == 0) mbar_wait(&sm.drain, 0);  // bounded; the MMAs drain before their TMEM is freed
+      __syncwarp();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+  } else {
+    // (the two sides share no code after the split of the registers)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ---------------- softmax: thread r owns row r of its stream's tile ----------------
     const int x = (warp - kSoftmaxWarp0) / 4;
     const int r = tid - (kSoftmaxWarp0 + 4 * x) * 32;
-    const int i = c.i0 + x * kRows + r;
+    const int row = (kSplit ? 0 : x * kRows) + r;  // row of the CTA
+    const int i = c.i0 + row;
     const uint32_t lane_base = (uint32_t)(((warp - kSoftmaxWarp0) & 3) * 32) << 16;
     const uint32_t s_cols = tmem + lane_base + (uint32_t)x * 128u;
-    const uint32_t o_cols = tmem + lane_base + kColO + (uint32_t)x * 128u;
+    const uint32_t o_cols = tmem + lane_base + kColO;  // O of stream A; B's is 128 columns on
     const int2 range = range_of(a, c.m, b, i, false);
-    RowScore rs;
-    rs.mul = kCap ? a.scale / a.softcap * 2.f * kLog2e : a.scale * kLog2e;
-    rs.cap2 = a.softcap * kLog2e;
-    rs.slope2 = 0.f;
+    const float mul = kCap ? a.scale / a.softcap : a.scale * kLog2e;
+    const float cap2 = a.softcap * kLog2e;
+    float slope2 = 0.f;
     int pos = 0, ref = 0;  // ref: the distance of the row's most favoured key, taken off all of them
     if (kBias) {
       const float slope = a.slopes[h];
-      rs.slope2 = slope * kLog2e;
+      slope2 = slope * kLog2e;
       pos = a.pos[b] + i;
       const bool pre = range.y > range.x;
       if (slope >= 0.f)
@@ -519,144 +706,189 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         ref = max(min(i + c.fill, c.n - 1), pre ? pos - range.x : 0);
     }
-    // l normalises O with the same bf16-rounded weights the MMA used; lu gives lse
-    float m_used = -INFINITY, l = 0.f, lu = 0.f;
-    int j = 0;  // key tiles this query tile has seen
+    // l sums the unrounded weights, for O and lse alike: where one key dominates, O is off by the
+    // rounding of its weight (at most half a bf16 step, as the output's own rounding); summing the
+    // rounded ones too cost three more instructions a score pair
+    float m_used = -INFINITY, l = 0.f;
+    int j = 0;  // key tiles this stream has seen
     bool ok = true;
-    for (int t = 0; t < total; ++t) {
+    for (int t = kSplit ? x : 0; t < total; t += kSplit ? 2 : 1) {
       int kind, start;
-      tile_kind(c, t, kind, start);
-      if (!tile_visible(c, x, kind, start)) continue;
+      tile_of(t, kind, start);
+      if (!kSplit && !tile_visible(c, x, kind, start)) continue;
       ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], j & 1, a.status));
       if (!ok) break;
       tc_fence_after();
-      // this row's visible columns of the tile
-      int lo = 0, hi = 0, base = 0;
-      if (kind == kPrefix) {
-        lo = range.x - start;
-        hi = range.y - start;
-        base = pos - start - ref;
-      } else if (kind == kBand) {
-        lo = i - c.n + 1 - start;
-        hi = min(i, c.T - 1) + 1 - start;
-        base = i - start - ref;
-      } else {
-        base = i - ref;
+      uint32_t raw[4][32];
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_cols + (uint32_t)ch * 32u, raw[ch]);
+      const RowTile rt = row_tile(c, kind, start, i, range, pos, ref);
+      const bool full = __all_sync(0xffffffffu, rt.lo <= 0 && rt.hi >= kRows);
+      tmem_wait_ld();
+      float s[kRows];
+#pragma unroll
+      for (int e = 0; e < kRows; ++e) s[e] = __uint_as_float(raw[e / 32][e % 32]);
+      score_row<kCap, kBias>(s, rt, full, mul, cap2, slope2, c.n);
+      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kRows; e += 8) {
+        m0 = max3(m0, s[e], s[e + 1]);
+        m1 = max3(m1, s[e + 2], s[e + 3]);
+        m2 = max3(m2, s[e + 4], s[e + 5]);
+        m3 = max3(m3, s[e + 6], s[e + 7]);
       }
-      const bool full = kind != kRing && __all_sync(0xffffffffu, lo <= 0 && hi >= kRows);
-      // pass 1: the row's maximum
-      float m0 = -INFINITY, m1 = -INFINITY;
-      const bool raw_max = full && !kBias;  // the scale and the cap keep the order
-#pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t rr[32];
-        tmem_ld32(s_cols + (uint32_t)ch * 32u, rr);
-        tmem_wait_ld();
-        if (raw_max) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            m0 = max3(m0, __uint_as_float(rr[e]), __uint_as_float(rr[e + 1]));
-            m1 = max3(m1, __uint_as_float(rr[e + 2]), __uint_as_float(rr[e + 3]));
-          }
-        } else {
-          float xv[32];
-          score_chunk<kCap, kBias>(c, rs, kind, start, ch * 32, lo, hi, i, base, full, rr, xv);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            m0 = max3(m0, xv[e], xv[e + 1]);
-            m1 = max3(m1, xv[e + 2], xv[e + 3]);
-          }
-          // pass 2 finds them scored
-#pragma unroll
-          for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(xv[e]);
-          tmem_st32(s_cols + (uint32_t)ch * 32u, rr);
-        }
-      }
-      float tmax = fmaxf(m0, m1);
-      if (raw_max) tmax = scored<kCap>(rs, tmax);
-      else tmem_wait_st();
+      float tmax = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+      if (!kCap && !kBias) tmax *= mul;  // still raw scores: the scale is positive
       const bool rescale = tmax > m_used + kLazyRescaleLog2;
       float alpha = 1.f;
       if (rescale) {
         alpha = ex2(m_used - tmax);
         l *= alpha;
-        lu *= alpha;
         m_used = tmax;
       }
+      // the previous P V of this stream is done (the commit that completed S covers it)
       if (j > 0 && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t rr[32];
-          tmem_ld32(o_cols + (uint32_t)ch * 32u, rr);
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t rr[16];
+          tmem_ld16(o_cols + (uint32_t)(x * 128 + ch * 16), rr);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
-          tmem_st32(o_cols + (uint32_t)ch * 32u, rr);
+          for (int e = 0; e < 16; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+          tmem_st16(o_cols + (uint32_t)(x * 128 + ch * 16), rr);
         }
       }
       const float m_sub = m_used == -INFINITY ? 0.f : m_used;
-      float2 lsum = make_float2(0.f, 0.f), lusum = make_float2(0.f, 0.f);
-#pragma unroll 1
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll
       for (int ch = 0; ch < 4; ++ch) {
-        uint32_t rr[32];
-        tmem_ld32(s_cols + (uint32_t)ch * 32u, rr);
-        tmem_wait_ld();
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float2 s2 = make_float2(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1]));
-          if (raw_max) s2 = make_float2(scored<kCap>(rs, s2.x), scored<kCap>(rs, s2.y));
-          const float2 p2 = make_float2(ex2(s2.x - m_sub), ex2(s2.y - m_sub));
+          float2 z2 = make_float2(s[32 * ch + 2 * e], s[32 * ch + 2 * e + 1]);
+          z2 = (!kCap && !kBias) ? __ffma2_rn(z2, splat(mul), splat(-m_sub)) : __fadd2_rn(z2, splat(-m_sub));
+          const float2 p2 = make_float2(ex2(z2.x), ex2(z2.y));
           const __nv_bfloat162 pb = __floats2bfloat162_rn(p2.x, p2.y);
           pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
-          lsum = __fadd2_rn(lsum, make_float2(__uint_as_float(pk[e] << 16), __uint_as_float(pk[e] & 0xffff0000u)));
-          lusum = __fadd2_rn(lusum, p2);
+          if (e & 1)
+            sum1 = __fadd2_rn(sum1, p2);
+          else
+            sum0 = __fadd2_rn(sum0, p2);
         }
         tmem_st16(s_cols + (uint32_t)ch * 16u, pk);
       }
-      l += lsum.x + lsum.y;
-      lu += lusum.x + lusum.y;
+      l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sm.p_full[x]);
       ++j;
     }
     if (ok && j > 0) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (j - 1) & 1, a.status));
-    if (ok && j > 0) {
-      tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum stays one)
-      uint4* orow = reinterpret_cast<uint4*>(a.out + (bh * a.T + i) * kHeadDim);
+    const float lse_ref = kBias ? slope2 * (float)ref : 0.f;
+    if (!kSplit) {
+      if (ok && j > 0) {
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum stays one)
+        uint4* orow = reinterpret_cast<uint4*>(a.out + (bh * a.T + i) * kHeadDim);
 #pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t rr[32];
-        tmem_ld32(o_cols + (uint32_t)ch * 32u, rr);
-        tmem_wait_ld();
-        if (i < c.T) {
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t rr[32];
+          tmem_ld32(o_cols + (uint32_t)(x * 128 + ch * 32), rr);
+          tmem_wait_ld();
+          if (i < c.T) {
+            float o[32];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(rr[e]) * inv;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const __nv_bfloat162 o2 = __floats2bfloat162_rn(__uint_as_float(rr[e + 2 * u]) * inv,
-                                                              __uint_as_float(rr[e + 2 * u + 1]) * inv);
-              w[u] = *reinterpret_cast<const uint32_t*>(&o2);
-            }
-            orow[ch * 4 + e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 4; ++e) orow[ch * 4 + e] = to_bf16x8(o + 8 * e);
           }
         }
+        if (i < c.T && a.lse) a.lse[bh * a.T + i] = l == 0.f ? -INFINITY : (m_used + log2f(l) - lse_ref) * kLn2;
       }
-      if (i < c.T && a.lse)
-        a.lse[bh * a.T + i] = lu == 0.f ? -INFINITY : (m_used + log2f(lu) - rs.slope2 * (float)ref) * kLn2;
+    } else {
+      // ---- the two streams' parts of the row meet; each group takes half of the columns ----
+      sm.stat_m[x][r] = m_used;
+      sm.stat_l[x][r] = l;
+      tc_fence_before();
+      softmax_barrier();  // all 256 threads come here, also after a give-up
+      tc_fence_after();
+      const float ma = sm.stat_m[0][r], mb = sm.stat_m[1][r];
+      const float M = fmaxf(ma, mb), m_sub = M == -INFINITY ? 0.f : M;
+      const bool none = total < 1, one = total < 2;  // streams without a key tile have no O
+      const float fa = none ? 0.f : ex2(ma - m_sub), fb = one ? 0.f : ex2(mb - m_sub);
+      const float L = fmaf(sm.stat_l[1][r], fb, sm.stat_l[0][r] * fa);
+      const float inv = cluster > 1 ? 1.f : (L == 0.f ? 0.f : 1.f / L);
+      float* part = reinterpret_cast<float*>(sm.k[0]) + r * kPartStride;  // every copy and MMA of the CTA is done
+      uint4* orow = reinterpret_cast<uint4*>(a.out + (bh * a.T + i) * kHeadDim);
+#pragma unroll 1
+      for (int ch = 0; ch < 2; ++ch) {
+        const int col = x * 64 + ch * 32;
+        uint32_t ra[32], rb[32];
+        if (!none) tmem_ld32(o_cols + (uint32_t)col, ra);
+        if (!one) tmem_ld32(o_cols + 128u + (uint32_t)col, rb);
+        tmem_wait_ld();
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          o[e] = none ? 0.f : __uint_as_float(ra[e]) * fa;
+          if (!one) o[e] = fmaf(__uint_as_float(rb[e]), fb, o[e]);
+          o[e] *= inv;
+        }
+        if (cluster > 1) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + col + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else if (i < c.T) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) orow[col / 8 + e] = to_bf16x8(o + 8 * e);
+        }
+      }
+      if (cluster == 1) {
+        if (x == 0 && i < c.T && a.lse) a.lse[bh * a.T + i] = L == 0.f ? -INFINITY : (M + log2f(L) - lse_ref) * kLn2;
+      } else {
+        softmax_barrier();  // both groups have read the streams' values
+        if (x == 0) {
+          sm.stat_m[0][r] = M;
+          sm.stat_l[0][r] = L;
+          sm.stat_l[1][r] = lse_ref;
+        }
+        // ---- the cluster's parts meet: CTA `rank` joins rows [rank, rank + 1) * 128 / cluster ----
+        cluster_sync();  // every CTA of the cluster comes here, also after a give-up
+        const int rows = kRows / cluster;
+        for (int v = tid - kSoftmaxWarp0 * 32; v < rows * (kHeadDim / 8); v += 256) {
+          const int r2 = rank * rows + v / (kHeadDim / 8), d = v % (kHeadDim / 8) * 8, i2 = c.i0 + r2;
+          if (i2 >= c.T) continue;
+          float ms[kMaxCluster], Mc = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < kMaxCluster; ++u) {
+            ms[u] = u < cluster ? peer_f32(peer_smem(&sm.stat_m[0][r2], u)) : -INFINITY;
+            Mc = fmaxf(Mc, ms[u]);
+          }
+          const float mc_sub = Mc == -INFINITY ? 0.f : Mc;
+          float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, Lc = 0.f;
+#pragma unroll
+          for (int u = 0; u < kMaxCluster; ++u) {
+            if (u >= cluster) break;
+            const float f = exp2f(ms[u] - mc_sub);
+            Lc = fmaf(peer_f32(peer_smem(&sm.stat_l[0][r2], u)), f, Lc);
+            const uint32_t at = peer_smem(reinterpret_cast<const float*>(sm.k[0]) + r2 * kPartStride + d, u);
+            const float4 p = peer_f32x4(at), q = peer_f32x4(at + 16);
+            o[0] = fmaf(p.x, f, o[0]), o[1] = fmaf(p.y, f, o[1]), o[2] = fmaf(p.z, f, o[2]), o[3] = fmaf(p.w, f, o[3]);
+            o[4] = fmaf(q.x, f, o[4]), o[5] = fmaf(q.y, f, o[5]), o[6] = fmaf(q.z, f, o[6]), o[7] = fmaf(q.w, f, o[7]);
+          }
+          const float inv_c = Lc == 0.f ? 0.f : 1.f / Lc;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] *= inv_c;
+          reinterpret_cast<uint4*>(a.out + (bh * a.T + i2) * kHeadDim)[d / 8] = to_bf16x8(o);
+          if (d == 0 && a.lse)
+            a.lse[bh * a.T + i2] = Lc == 0.f ? -INFINITY : (Mc + log2f(Lc) - sm.stat_l[1][r2]) * kLn2;
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA's shared memory goes away while another reads it
+      }
     }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) {
-    if (lane == 0) mbar_wait(&sm.drain, 0);  // bounded; the MMAs drain before their TMEM is freed
-    __syncwarp();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    tc_fence_before();
+    __syncthreads();
   }
 }
 
@@ -726,16 +958,37 @@ cudaError_t launch_scored_prefill(const ScoredPrefillLaunch& L, cudaStream_t str
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;
   a.status = L.status;
+  // Paired CTAs where 256-row tiles fill the SMs; below that split ones of 128 rows, and clusters as
+  // large as the SMs and the key tiles allow.
+  const int sms = device_sm_count();
+  const int64_t pairs = (int64_t)((L.T + kMaxRows - 1) / kMaxRows) * bh, tiles = (int64_t)((L.T + kRows - 1) / kRows) * bh;
+  const bool split = pairs < sms;
+  const int64_t keys = (L.cap + kRows - 1) / kRows + (L.n + kRows - 1) / kRows;  // at most, for a query tile
+  a.cluster = 1;
+  while (split && a.cluster < kMaxCluster && tiles * a.cluster * 2 <= sms && keys >= 4 * a.cluster) a.cluster *= 2;
   const bool cap = L.softcap > 0.f, bias = L.slopes != nullptr;
-  auto kernel = cap ? (bias ? scored_prefill_kernel<true, true> : scored_prefill_kernel<true, false>)
-                    : (bias ? scored_prefill_kernel<false, true> : scored_prefill_kernel<false, false>);
-  static unsigned long long done[4] = {};
-  const size_t smem = sizeof(Smem) + 1024;
-  if ((e = ensure_smem_limit(kernel, smem, &done[2 * cap + bias])) != cudaSuccess) return e;
-  const dim3 grid((L.T + kCtaRows - 1) / kCtaRows, L.H, L.B);
+  auto kernel = split ? (cap ? (bias ? scored_prefill_kernel<true, true, true> : scored_prefill_kernel<true, false, true>)
+                             : (bias ? scored_prefill_kernel<false, true, true> : scored_prefill_kernel<false, false, true>))
+                      : (cap ? (bias ? scored_prefill_kernel<true, true, false> : scored_prefill_kernel<true, false, false>)
+                             : (bias ? scored_prefill_kernel<false, true, false> : scored_prefill_kernel<false, false, false>));
+  static unsigned long long done[8] = {}, checked[8] = {};
+  const int which = 4 * split + 2 * cap + bias;
+  const size_t smem = sizeof(Smem);
+  if ((e = ensure_smem_limit(kernel, smem, &done[which])) != cudaSuccess) return e;
+  if (!__atomic_load_n(&checked[which], __ATOMIC_ACQUIRE)) {  // the register split draws on the launch's
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+    if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+    __atomic_store_n(&checked[which], 1ull, __ATOMIC_RELEASE);
+  }
+  const dim3 grid(split ? (L.T + kRows - 1) / kRows * a.cluster : (L.T + kMaxRows - 1) / kMaxRows, L.H, L.B);
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   fill_launch_config(cfg, attr, grid, dim3(kThreads), smem, stream);
+  attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+  attr[cfg.numAttrs].val.clusterDim.x = a.cluster;
+  attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+  ++cfg.numAttrs;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, a, tq, tko, tvo, tpk, tpv, trk, trv)) != cudaSuccess) return e;
   if (!L.write_ring) return cudaSuccess;
   fill_launch_config(cfg, attr, dim3(L.H, L.B), dim3(256), 0, stream);

@@ -93,6 +93,8 @@ class Case:
     (1, 1, 1, 1, 1, None), (1, 1, 1, 1, 1, [1]), (1, 2, 5, 127, 7, [3]), (2, 1, 128, 128, 128, [128, 0]),
     (1, 2, 129, 129, 128, [77]), (2, 2, 257, 300, 100, [100, 1]), (1, 1, 700, 1000, 300, [299]),
     (1, 1, 300, 500, 1024, [1000]), (2, 3, 64, 2592, 128, None),
+    (1, 1, 10, 5000, 128, [128]), (1, 3, 130, 2000, 64, [9]),   # one query tile's keys over a cluster
+    (5, 16, 300, 400, 128, [128, 0, 64, 1, 127]),               # more 256-query tiles than SMs
 ])
 @pytest.mark.parametrize("softcap,bias", [(0.0, False), (20.0, False), (0.0, True), (50.0, True)])
 def test_matches_plain_attention(cuda_lib, B, H, T, cap, n, fill, softcap, bias):
@@ -120,6 +122,33 @@ def test_documents(cuda_lib, softcap, bias):
     c = Case(4, 2, T, cap, ranges=ranges, fill=[128, 5, 0, 128], softcap=softcap, slopes=slopes_of(2) if bias else None,
              pos=[1500, 1700, 1500, 40000] if bias else None, seed=50)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), (30.0, True)])
+def test_documents_of_many_sequences(cuda_lib, softcap, bias):
+    # as many 256-query tiles as the chip takes at once: tiles of queries share their key tiles
+    B, T, cap = 12, 300, 700
+    cuts = [0, 100, 101, 400, 650, 700]
+    orders = [[0, 1, 2, 3, 4], [4, 0, 3, 1, 2], [2, 2, 2, 2, 2], [3, 0, 3, 0, 3]]
+    c = Case(B, 16, T, cap, ranges=[documents(T, cuts, orders[b % 4], 61 + b) for b in range(B)],
+             fill=[(11 * b) % 129 for b in range(B)], softcap=softcap, slopes=slopes_of(16) if bias else None,
+             pos=[700 + b for b in range(B)] if bias else None, seed=60)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("qscale", [1.0, 4.0, 30.0])
+@pytest.mark.parametrize("softcap", [5.0, 20.0, 1000.0])
+def test_caps_from_barely_to_fully_saturated(cuda_lib, softcap, qscale):
+    # |scale q.k| / cap from 0.01 to 50: both polynomials and the exponential form, within one warp too
+    c = Case(1, 2, 150, 300, softcap=softcap, fill=[100], qstd=qscale, seed=61)
+    c.q[:, :, ::3] *= 0.05
+    out, lse = c.run()
+    # a score of s errs by at most 2^-20 sum |q k| scale before the cap, which only shrinks it
+    extra = 2.0 ** -20 * qscale * 2 * math.sqrt(D) if softcap == 1000.0 else 0.0
+    if extra < 1e-4:
+        c.check(out, lse, rel=8e-3)
+    else:
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
 
 
 def test_what_lies_outside_the_documents_stays_there(cuda_lib):

@@ -12,8 +12,8 @@
 //     cluster of up to 8 CTAs deals the key tiles out among its CTAs; the parts meet through shared
 //     memory, the CTAs' through distributed shared memory.
 // While one stream's softmax runs, the tensor core works on the other's products. Roles: warp 0 TMA
-// producer of Q and K, warp 2 of V, warp 1 MMA issuer, warps 4-7 / 8-11 softmax of stream A / B, thread r
-// owning row r: its 128 scores are read from TMEM once and stay in registers (the softmax warps take
+// producer of Q and K, warp 2 of V, warp 3 cleans V, one thread of warp 1 issues the MMAs, warps 4-7 / 8-11
+// softmax of stream A / B, thread r owning row r: its 128 scores are read from TMEM once and stay in registers (the softmax warps take
 // the registers that the others give up), and P (bf16) goes back over S as the A operand of P V.
 //
 // Documents: the union of the rows' ranges, as up to four runs of rows, gives the prefix tiles;
@@ -77,11 +77,12 @@ struct __align__(1024) Smem {
   uint8_t v[kVStages][kTileBytes];
   uint64_t q_full;
   uint64_t k_full[kKStages], k_empty[kKStages];
-  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t v_full[kVStages], v_ready[kVStages], v_empty[kVStages];
   uint64_t s_full[kQTiles], p_full[kQTiles], o_done[kQTiles];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  int seen_by[kKStages];  // with a key tile: the streams that see it, as bits
   Ctx ctx;
   float stat_m[2][kRows];  // split: the streams' maxima,
   float stat_l[2][kRows];  // and sums; [0] then holds the CTA's
@@ -175,6 +176,12 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
@@ -374,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_ready[s], 1);
       mbar_init(&sm.v_empty[s], 1);
     }
     for (int x = 0; x < kQTiles; ++x) {
@@ -498,15 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Ctx& c = sm.ctx;
   const uint32_t tmem = sm.tmem_base;
   const int total = c.total;
-  // this CTA's t-th key tile, and what stream x does with it
+  // this CTA's t-th key tile
   auto tile_of = [&](int t, int& kind, int& start) { tile_kind(c, kSplit ? t * cluster + rank : t, kind, start); };
-  auto has = [&](int x, int t) {
-    if (kSplit) return (t & 1) == x;
-    int kind, start;
-    tile_kind(c, t, kind, start);
-    return tile_visible(c, x, kind, start);
-  };
-
   if (warp < kSoftmaxWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     if (warp == 0 || warp == 2) {
@@ -535,6 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t rows = kind == kPrefix ? a.cap : (kind == kRing ? a.n : a.T);
           const int row = (int)(bh * rows) + start;
           uint8_t* dst = is_k ? sm.k[s] : sm.v[s];
+          if (is_k && !kSplit)  // released by the arrival below
+            sm.seen_by[s] = (tile_visible(c, 0, kind, start) ? 1 : 0) | (tile_visible(c, 1, kind, start) ? 2 : 0);
           mbar_arrive_expect_tx(&full[s], kTileBytes);
           tma_load_2d(dst, map, 0, row, &full[s]);
           tma_load_2d(dst + kRegionBytes, map, 64, row, &full[s]);
@@ -545,64 +548,116 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 1) {
-      // ---------------- MMA issuer (lane 0) + V-row zeroing (whole warp) ----------------
-      constexpr uint32_t kIdescQK = idesc_bf16_m128_n128(0);
-      constexpr uint32_t kIdescPV = idesc_bf16_m128_n128(1);
-      int n_pv[kQTiles] = {0, 0};
-      int k_ready = 0;  // key tiles waited for
-      bool ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.q_full, 0, a.status));
-      tc_fence_after();
-      auto wait_k = [&](int t) {  // key tiles up to t have landed
-        for (; k_ready <= t; ++k_ready) {
-          if (!__all_sync(0xffffffffu,
-                          wait_or_abort(sm, &sm.k_full[k_ready % kKStages], (k_ready / kKStages) & 1, a.status)))
-            return false;
-          tc_fence_after();
-        }
-        return true;
-      };
-      auto issue_s = [&](int x, int t) {  // S_x = Q K_t^T
-        if (lane == 0) {
-          const uint32_t q_addr = smem_addr(sm.q[kSplit ? 0 : x]);
-          const uint32_t k_addr = smem_addr(sm.k[t % kKStages]);
+      // ---------------- MMA issuer: one thread ----------------
+      // The tensor core's queue is two or three MMAs deep: issuing blocks for about as long as they
+      // run, and whatever else this thread does leaves the tensor core idle. So it waits, issues and
+      // commits, and others look tiles up (warp 0) and clean V (warp 3).
+      if (elect_one()) {
+        constexpr uint32_t kIdescQK = idesc_bf16_m128_n128(0);
+        constexpr uint32_t kIdescPV = idesc_bf16_m128_n128(1);
+        const uint64_t q_desc = smem_desc_sw128(smem_addr(sm.q[0]), 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(smem_addr(sm.k[0]), 16, 1024);
+        const uint64_t v_desc = smem_desc_sw128(smem_addr(sm.v[0]), kRegionBytes, 1024);
+        auto issue_s = [&](int x, int ks) {  // S_x = Q K^T
+          const uint64_t q = q_desc + (uint64_t)((kSplit ? 0 : x) * (kTileBytes >> 4)), k = k_desc + (uint64_t)(ks * (kTileBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (uint32_t)(kk >> 2) * kRegionBytes + (uint32_t)(kk & 3) * 32u;
-            tc_mma_ss(tmem + (uint32_t)x * 128u, smem_desc_sw128(q_addr + off, 16, 1024),
-                      smem_desc_sw128(k_addr + off, 16, 1024), kIdescQK, kk > 0);
+            const uint64_t off = (uint64_t)(((kk >> 2) * kRegionBytes + (kk & 3) * 32) >> 4);
+            tc_mma_ss(tmem + (uint32_t)x * 128u, q + off, k + off, kIdescQK, kk > 0);
           }
           tc_commit(&sm.s_full[x]);
-        }
-        __syncwarp();
-      };
-      auto free_k = [&](int t) {
-        if (lane == 0) tc_commit(&sm.k_empty[t % kKStages]);
-        __syncwarp();
-      };
-      constexpr int kAhead = kSplit ? 2 : 1;  // a stream's next key tile
-      if (ok && kSplit) {
-        for (int t = 0; ok && t < min(2, total); ++t)
-          if ((ok = wait_k(t))) {
-            issue_s(t, t);
-            free_k(t);
+        };
+        auto issue_pv = [&](int x, int vs, bool more) {  // O_x += P_x V
+          const uint64_t v = v_desc + (uint64_t)(vs * (kTileBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_ts(tmem + kColO + (uint32_t)x * 128u, tmem + (uint32_t)x * 128u + (uint32_t)kk * 8u,
+                      v + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (more || kk > 0) ? 1u : 0u);
+          tc_commit(&sm.o_done[x]);
+        };
+        bool ok = wait_or_abort(sm, &sm.q_full, 0, a.status);
+        uint32_t p_phase[kQTiles] = {0, 0};
+        bool more[kQTiles] = {false, false};
+        int ks = 0, vs = 0;
+        uint32_t k_phase = 0, v_phase = 0;
+        auto take_k = [&](int& seen) {  // the next key tile has landed
+          if (!wait_or_abort(sm, &sm.k_full[ks], k_phase, a.status)) return false;
+          tc_fence_after();
+          if (!kSplit) seen = *reinterpret_cast<volatile int*>(&sm.seen_by[ks]);
+          return true;
+        };
+        auto free_k = [&]() {
+          tc_commit(&sm.k_empty[ks]);
+          if (++ks == kKStages) {
+            ks = 0;
+            k_phase ^= 1;
           }
-      } else if (ok && (ok = wait_k(0))) {
-        for (int x = 0; x < kQTiles; ++x)
-          if (has(x, 0)) issue_s(x, 0);
-        free_k(0);
+        };
+        int seen = 0, seen_next = 0;
+        if (kSplit) {
+          for (int t = 0; ok && t < min(2, total); ++t)
+            if ((ok = take_k(seen))) {
+              issue_s(t, ks);
+              free_k();
+            }
+        } else if (ok && (ok = take_k(seen))) {
+          if (seen & 1) issue_s(0, ks);
+          if (seen & 2) issue_s(1, ks);
+          free_k();
+        }
+        for (int t = 0; ok && t < total; ++t) {
+          if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a.status))) break;
+          if (kSplit) {
+            const int x = t & 1;
+            if (!(ok = wait_or_abort(sm, &sm.p_full[x], (t >> 1) & 1, a.status))) break;
+            tc_fence_after();
+            issue_pv(x, vs, t > 1);
+            tc_commit(&sm.v_empty[vs]);
+            if (t + 2 < total) {
+              if (!(ok = take_k(seen))) break;
+              issue_s(x, ks);
+              free_k();
+            }
+          } else {
+            const bool next = t + 1 < total;
+#pragma unroll
+            for (int x = 0; x < kQTiles; ++x) {
+              if (seen >> x & 1) {
+                if (!(ok = wait_or_abort(sm, &sm.p_full[x], p_phase[x], a.status))) break;
+                p_phase[x] ^= 1;
+                tc_fence_after();
+                issue_pv(x, vs, more[x]);
+                more[x] = true;
+              }
+              if (x == 0 && next && !(ok = take_k(seen_next))) break;
+              if (x == 1) tc_commit(&sm.v_empty[vs]);
+              if (next && (seen_next >> x & 1)) issue_s(x, ks);
+            }
+            if (!ok) break;
+            if (next) free_k();
+            seen = seen_next;
+          }
+          if (++vs == kVStages) {
+            vs = 0;
+            v_phase ^= 1;
+          }
+        }
+        tc_commit(&sm.drain);  // fires once every issued MMA is done
       }
+    } else {
+      // ---------------- V rows that no query of the CTA sees: zeroed (whole warp) ----------------
+      bool ok = true;
       for (int t = 0; ok && t < total; ++t) {
         const int vs = t % kVStages;
-        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[vs], (t / kVStages) & 1, a.status));
-        if (!ok) break;
         int kind, start;
         tile_of(t, kind, start);
-        bool zeroed = false;
         // a prefix tile inside one run is seen whole
         bool whole = kind == kBand && start + kRows <= c.T;
         if (kind == kPrefix)
           for (int r = 0; r < c.runs; ++r)
             whole |= start >= c.lo[r] && start + kRows <= c.hi[r] && (c.exact || r < kRuns - 1);
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[vs], (t / kVStages) & 1, a.status));
+        if (!ok) break;
         if (!whole) {
           for (int r = lane; r < kRows; r += 32) {
             const int x = start + r;
@@ -627,46 +682,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 row0[e] = make_uint4(0, 0, 0, 0);
                 row1[e] = make_uint4(0, 0, 0, 0);
               }
-              zeroed = true;
             }
           }
-          if (__any_sync(0xffffffffu, zeroed)) fence_async_smem();
+          fence_async_smem();
           __syncwarp();
         }
-        const bool next = t + kAhead < total;
-        for (int x = 0; ok && x < kQTiles; ++x) {
-          if (has(x, t)) {
-            ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.p_full[x], n_pv[x] & 1, a.status));
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t v_addr = smem_addr(sm.v[vs]);
-              const uint32_t p_tmem = tmem + (uint32_t)x * 128u;
-              const uint32_t o_tmem = tmem + kColO + (uint32_t)x * 128u;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_ts(o_tmem, p_tmem + (uint32_t)kk * 8u,
-                          smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, kRegionBytes, 1024), kIdescPV,
-                          (n_pv[x] > 0 || kk > 0) ? 1u : 0u);
-              tc_commit(&sm.o_done[x]);
-            }
-            __syncwarp();
-            ++n_pv[x];
-          }
-          if (next && has(x, t + kAhead)) {
-            if (!(ok = wait_k(t + kAhead))) break;
-            issue_s(x, t + kAhead);
-          }
-        }
-        if (!ok) break;
-        if (lane == 0) tc_commit(&sm.v_empty[vs]);
-        if (next) {
-          if (!(ok = wait_k(t + kAhead))) break;  // also where no stream needed it: the copy lands before its stage is freed
-          free_k(t + kAhead);
-        }
-        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_ready[vs]);
       }
-      if (lane == 0) tc_commit(&sm.drain);  // fires once every issued MMA is done
     }
     __syncwarp();
     if (kSplit && cluster > 1) {

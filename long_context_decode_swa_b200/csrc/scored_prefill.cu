@@ -101,6 +101,8 @@ struct Args {
   const int32_t* pos;
   float softcap, scale;
   int cluster;            // split: CTAs that share a query tile's key tiles
+  int first;              // split: the first pair of query tiles that is this launch's
+  int late;               // the launch before this one is its own first part: waited for at the end
   __nv_bfloat16* out;
   float* lse;
   int32_t* status;
@@ -172,6 +174,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -186,18 +194,38 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 
-// u -> cap2 tanh(u), u = raw k, for pairs: minimax polynomials (error 2e-8 of tanh on their range).
-template <int kTerms>
-__device__ __forceinline__ float2 tanh_poly(float2 raw, float k, const float (&coef)[kTerms], float cap2) {
+// tanh(u) = u p(u^2): minimax polynomials, within 2e-8 for |u| up to 0.4 and up to 1 (four and seven terms).
+constexpr float kTanhSmall = 0.4f, kTanhMid = 1.f;
+struct TanhSmall {
+  static constexpr int kTerms = 4;
+  static __device__ __forceinline__ float coef(int i) {
+    constexpr float c[kTerms] = {0.999999573f, -0.333297261f, 0.132505672f, -0.0468257397f};
+    return c[i];
+  }
+};
+struct TanhMid {
+  static constexpr int kTerms = 7;
+  static __device__ __forceinline__ float coef(int i) {
+    constexpr float c[kTerms] = {0.999999693f,  -0.333321293f,   0.133195837f,  -0.0532658353f,
+                                 0.0199732827f, -0.00595128048f, 0.000963772187f};
+    return c[i];
+  }
+};
+
+// cap2 tanh(raw k) + add, for a pair.
+template <typename Poly>
+__device__ __forceinline__ float2 capped_pair(float2 raw, float k, float cap2, float2 add) {
   const float2 u = __fmul2_rn(raw, splat(k));
   const float2 w = __fmul2_rn(u, u);
-  float2 p = splat(coef[kTerms - 1] * cap2);
+  float2 p = splat(Poly::coef(Poly::kTerms - 1) * cap2);
 #pragma unroll
-  for (int i = kTerms - 2; i >= 0; --i) p = __ffma2_rn(p, w, splat(coef[i] * cap2));
-  return __fmul2_rn(u, p);
+  for (int i = Poly::kTerms - 2; i >= 0; --i) p = __ffma2_rn(p, w, splat(Poly::coef(i) * cap2));
+  return __ffma2_rn(u, p, add);
 }
 
-constexpr float kTanhSmall = 0.6f, kTanhMid = 1.f;
+__device__ __forceinline__ float capped_exact(float raw, float k, float cap2) {
+  return fmaf(-2.f * cap2, rcp(ex2(raw * (k * 2.f * kLog2e)) + 1.f), cap2);
+}
 
 // Visible columns [lo, hi) of a tile as bits of its w-th 32 columns.
 __device__ __forceinline__ uint32_t column_bits(int lo, int hi, int w) {
@@ -240,72 +268,83 @@ __device__ __forceinline__ RowTile row_tile(const Ctx& c, int kind, int start, i
   return t;
 }
 
-// Raw scores -> scores in the log2 domain, masked ones -inf. k: scale / cap, or scale log2(e) without a
-// cap; full (uniform over the warp): nothing is masked.
+// How a warp takes the tanh of some scores: by the largest |u| among its rows'.
+enum Tanh { kSmall, kMid, kExact };
+
+__device__ __forceinline__ Tanh tanh_of(float lowest, float highest, float k) {
+  const float u = fmaxf(highest, -lowest) * k;
+  if (__all_sync(0xffffffffu, u <= kTanhSmall)) return kSmall;
+  return __all_sync(0xffffffffu, u <= kTanhMid) ? kMid : kExact;
+}
+
+__device__ __forceinline__ float highest_of(const float (&x)[32], float a) {
+  float b = a;
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    a = max3(a, x[e], x[e + 1]);
+    b = max3(b, x[e + 2], x[e + 3]);
+  }
+  return fmaxf(a, b);
+}
+
+__device__ __forceinline__ float lowest_of(const float (&x)[32], float a) {
+  float b = a;
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    a = min3(a, x[e], x[e + 1]);
+    b = min3(b, x[e + 2], x[e + 3]);
+  }
+  return fminf(a, b);
+}
+
+// Raw scores of a tile's columns [col0, col0 + 32) -> scores in the log2 domain, masked ones -inf.
+// k: scale / cap, or scale log2(e) without a cap; full (uniform over the warp): nothing is masked.
 template <bool kCap, bool kBias>
-__device__ __forceinline__ void score_row(float (&x)[kRows], const RowTile& t, bool full, float k, float cap2, float slope2,
-                                          int n) {
-  if (kCap) {
-    float a0 = 0.f, a1 = 0.f;
+__device__ __forceinline__ void score_chunk(float (&x)[32], const RowTile& t, int col0, bool full, float k, float cap2,
+                                            float slope2, int n) {
+  // -slope (base - e) = slope e + c0: exact integers, one rounding of the bias
+  const float c0 = kBias ? -slope2 * (float)(t.base - col0) : 0.f;
+  auto bias = [&](int e) {
+    // (not paired: a pair of constants would take two moves, one is an immediate operand)
+    return kBias ? make_float2(fmaf(slope2, (float)e, c0), fmaf(slope2, (float)(e + 1), c0)) : make_float2(0.f, 0.f);
+  };
+  const Tanh how = kCap ? tanh_of(lowest_of(x, INFINITY), highest_of(x, -INFINITY), k) : kSmall;
+  if (kCap && how == kExact) {
 #pragma unroll
-    for (int e = 0; e < kRows; e += 4) {
-      a0 = max3(a0, fabsf(x[e]), fabsf(x[e + 1]));
-      a1 = max3(a1, fabsf(x[e + 2]), fabsf(x[e + 3]));
+    for (int e = 0; e < 32; e += 2) {
+      const float2 b = bias(e);
+      x[e] = capped_exact(x[e], k, cap2) + b.x;
+      x[e + 1] = capped_exact(x[e + 1], k, cap2) + b.y;
     }
-    const float u = fmaxf(a0, a1) * k;
-    if (__all_sync(0xffffffffu, u <= kTanhSmall)) {
-      const float coef[5] = {0.999999627f, -0.333312086f, 0.132992102f, -0.0516967431f, 0.0149769602f};
+  } else if (kCap && how == kMid) {
 #pragma unroll
-      for (int e = 0; e < kRows; e += 2) {
-        const float2 s2 = tanh_poly(make_float2(x[e], x[e + 1]), k, coef, cap2);
-        x[e] = s2.x;
-        x[e + 1] = s2.y;
-      }
-    } else if (__all_sync(0xffffffffu, u <= kTanhMid)) {
-      const float coef[7] = {0.999999693f,  -0.333321293f, 0.133195837f,  -0.0532658353f,
-                             0.0199732827f, -0.00595128048f, 0.000963772187f};
-#pragma unroll
-      for (int e = 0; e < kRows; e += 2) {
-        const float2 s2 = tanh_poly(make_float2(x[e], x[e + 1]), k, coef, cap2);
-        x[e] = s2.x;
-        x[e + 1] = s2.y;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kRows; ++e) x[e] = fmaf(-2.f * cap2, rcp(ex2(x[e] * (k * 2.f * kLog2e)) + 1.f), cap2);
+    for (int e = 0; e < 32; e += 2) {
+      const float2 s2 = capped_pair<TanhMid>(make_float2(x[e], x[e + 1]), k, cap2, bias(e));
+      x[e] = s2.x;
+      x[e + 1] = s2.y;
     }
-  } else if (kBias) {
+  } else {
 #pragma unroll
-    for (int e = 0; e < kRows; e += 2) {
-      const float2 s2 = __fmul2_rn(make_float2(x[e], x[e + 1]), splat(k));
+    for (int e = 0; e < 32; e += 2) {
+      float2 s2 = make_float2(x[e], x[e + 1]);
+      if (kCap)
+        s2 = capped_pair<TanhSmall>(s2, k, cap2, bias(e));
+      else
+        s2 = kBias ? __ffma2_rn(s2, splat(k), bias(e)) : __fmul2_rn(s2, splat(k));
       x[e] = s2.x;
       x[e + 1] = s2.y;
     }
   }
-  if (kBias) {
-    // -slope (base - e) = slope e + c0: exact integers, one rounding of the bias
-    const float c0 = -slope2 * (float)t.base;
-    if (t.cut >= kRows) {
+  if (kBias && t.cut < kRows) {  // the ring's wrap
+    const float wrap = -slope2 * (float)n;
 #pragma unroll
-      for (int e = 0; e < kRows; e += 2) {
-        const float2 b2 = __ffma2_rn(splat(slope2), make_float2((float)e, (float)(e + 1)), splat(c0));
-        const float2 s2 = __fadd2_rn(make_float2(x[e], x[e + 1]), b2);
-        x[e] = s2.x;
-        x[e + 1] = s2.y;
-      }
-    } else {
-      const float c1 = -slope2 * (float)(t.base + n);
-#pragma unroll
-      for (int e = 0; e < kRows; ++e) x[e] += fmaf(slope2, (float)e, e < t.cut ? c0 : c1);
-    }
+    for (int e = 0; e < 32; ++e) x[e] += col0 + e < t.cut ? 0.f : wrap;
   }
   if (!full) {
+    const int w = col0 / 32;
+    const uint32_t bits = column_bits(t.lo, t.hi, w) | column_bits(t.lo2, t.hi2, w);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t bits = column_bits(t.lo, t.hi, w) | column_bits(t.lo2, t.hi2, w);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) x[32 * w + e] = (bits >> e) & 1 ? x[32 * w + e] : -INFINITY;
-    }
+    for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1 ? x[e] : -INFINITY;
   }
 }
 
@@ -362,16 +401,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kCtaRows = kSplit ? kRows : kMaxRows;
   const int cluster = kSplit ? a.cluster : 1;
   const int rank = kSplit ? (int)cluster_rank() : 0;
-  const int qt = kSplit ? blockIdx.x / cluster : blockIdx.x;
-  const int h = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t bh = (int64_t)b * a.H + h;
+  // pairs of query tiles in order: a (sequence, head)'s side by side
+  const int pairs = (a.T + kMaxRows - 1) / kMaxRows;
+  const int unit = kSplit ? blockIdx.x / cluster : blockIdx.x;
+  const int pair = kSplit ? a.first + unit / 2 : unit;
+  const int64_t bh = pair / pairs;
+  const int b = (int)(bh / a.H), h = (int)(bh - (int64_t)b * a.H);
+  const int qt = kSplit ? pair % pairs * 2 + (unit & 1) : pair % pairs;
   if ((smem_addr(smem_raw) & 1023u) != 0) {  // it is, with no other shared memory in the kernel
     if (tid == 0) set_status(a.status, RSWA_DEVICE_PIPELINE);
     return;
   }
-  griddep_wait();
+  // A late launch's CTAs start when the last of the first part's have (they have waited for what came
+  // before both), and run beside them; what follows waits for this launch, so it waits for them.
+  if (!a.late) griddep_wait();
   griddep_launch_dependents();
+  if (kSplit && qt * kRows >= a.T) {  // the chunk ends in the first tile of the pair
+    if (a.late) griddep_wait();
+    return;
+  }
   if (tid == 0) {
     sm.abort_flag = 0;
     mbar_init(&sm.q_full, 1);
@@ -696,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_sync();
     }
     __syncthreads();
+    if (a.late) griddep_wait();
     if (warp == 1) {
       tc_fence_after();
       if (lane == 0) mbar_wait(&sm.drain, 0);  // bounded; the MMAs drain before their TMEM is freed
@@ -741,26 +791,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], j & 1, a.status));
       if (!ok) break;
       tc_fence_after();
-      uint32_t raw[4][32];
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_cols + (uint32_t)ch * 32u, raw[ch]);
       const RowTile rt = row_tile(c, kind, start, i, range, pos, ref);
-      const bool full = __all_sync(0xffffffffu, rt.lo <= 0 && rt.hi >= kRows);
-      tmem_wait_ld();
-      float s[kRows];
+      if (__all_sync(0xffffffffu, (rt.hi <= 0 || rt.lo >= kRows || rt.hi <= rt.lo) && rt.hi2 <= rt.lo2)) {
+        // no row of this warp sees a key of the tile
+        const uint32_t zero[16] = {};
 #pragma unroll
-      for (int e = 0; e < kRows; ++e) s[e] = __uint_as_float(raw[e / 32][e % 32]);
-      score_row<kCap, kBias>(s, rt, full, mul, cap2, slope2, c.n);
-      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < kRows; e += 8) {
-        m0 = max3(m0, s[e], s[e + 1]);
-        m1 = max3(m1, s[e + 2], s[e + 3]);
-        m2 = max3(m2, s[e + 4], s[e + 5]);
-        m3 = max3(m3, s[e + 6], s[e + 7]);
+        for (int ch = 0; ch < 4; ++ch) tmem_st16(s_cols + (uint32_t)ch * 16u, zero);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[x]);
+        ++j;
+        continue;
       }
-      float tmax = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-      if (!kCap && !kBias) tmax *= mul;  // still raw scores: the scale is positive
+      // The passes over the row's 128 scores go 32 columns at a time, through TMEM, in loops that are
+      // not unrolled: holding all 128 in registers made straight-line code of 20 to 40 KB a tile, which
+      // the instruction cache did not feed (a biased tile took 8,000 cycles instead of 2,000).
+      const bool full = __all_sync(0xffffffffu, rt.lo <= 0 && rt.hi >= kRows);
+      auto load = [&](int ch, float(&v)[32]) {
+        uint32_t raw[32];
+        tmem_ld32(s_cols + (uint32_t)ch * 32u, raw);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
+      };
+      Tanh how = kExact;
+      float lowest = INFINITY, highest = -INFINITY;
+      if (!kBias && full) {
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          float v[32];
+          load(ch, v);
+          highest = highest_of(v, highest);
+          if (kCap) lowest = lowest_of(v, lowest);
+        }
+        if (kCap) how = tanh_of(lowest, highest, mul);
+      }
+      // without a mask or a bias the raw maximum is the maximum, and the scoring joins the exponentials' loop
+      const bool fused = !kBias && full && (!kCap || how != kExact);
+      float tmax;
+      if (fused) {
+        tmax = kCap ? cap2 * tanhf(highest * mul) : highest * mul;
+      } else {
+        tmax = -INFINITY;
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          float v[32];
+          load(ch, v);
+          score_chunk<kCap, kBias>(v, rt, ch * 32, full, mul, cap2, slope2, c.n);
+          tmax = highest_of(v, tmax);
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e]);
+          tmem_st32(s_cols + (uint32_t)ch * 32u, w);
+        }
+        tmem_wait_st();
+      }
       const bool rescale = tmax > m_used + kLazyRescaleLog2;
       float alpha = 1.f;
       if (rescale) {
@@ -782,23 +867,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float m_sub = m_used == -INFINITY ? 0.f : m_used;
       float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+      auto weights = [&](auto&& less_m) {  // less_m: a pair of s -> score - m
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          float v[32];
+          load(ch, v);
+          uint32_t pk[16];
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 z2 = make_float2(s[32 * ch + 2 * e], s[32 * ch + 2 * e + 1]);
-          z2 = (!kCap && !kBias) ? __ffma2_rn(z2, splat(mul), splat(-m_sub)) : __fadd2_rn(z2, splat(-m_sub));
-          const float2 p2 = make_float2(ex2(z2.x), ex2(z2.y));
-          const __nv_bfloat162 pb = __floats2bfloat162_rn(p2.x, p2.y);
-          pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
-          if (e & 1)
-            sum1 = __fadd2_rn(sum1, p2);
-          else
-            sum0 = __fadd2_rn(sum0, p2);
+          for (int e = 0; e < 16; ++e) {
+            const float2 z2 = less_m(make_float2(v[2 * e], v[2 * e + 1]));
+            const float2 p2 = make_float2(ex2(z2.x), ex2(z2.y));
+            const __nv_bfloat162 pb = __floats2bfloat162_rn(p2.x, p2.y);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
+            if (e & 1)
+              sum1 = __fadd2_rn(sum1, p2);
+            else
+              sum0 = __fadd2_rn(sum0, p2);
+          }
+          tmem_st16(s_cols + (uint32_t)ch * 16u, pk);
         }
-        tmem_st16(s_cols + (uint32_t)ch * 16u, pk);
-      }
+      };
+      const float2 minus_m = splat(-m_sub);
+      if (!fused)
+        weights([&](float2 z) { return __fadd2_rn(z, minus_m); });
+      else if (!kCap)
+        weights([&](float2 z) { return __ffma2_rn(z, splat(mul), minus_m); });
+      else if (how == kSmall)
+        weights([&](float2 z) { return capped_pair<TanhSmall>(z, mul, cap2, minus_m); });
+      else
+        weights([&](float2 z) { return capped_pair<TanhMid>(z, mul, cap2, minus_m); });
       l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       tmem_wait_st();
       tc_fence_before();
@@ -980,39 +1077,50 @@ cudaError_t launch_scored_prefill(const ScoredPrefillLaunch& L, cudaStream_t str
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;
   a.status = L.status;
-  // Paired CTAs where 256-row tiles fill the SMs; below that split ones of 128 rows, and clusters as
-  // large as the SMs and the key tiles allow.
+  // Paired CTAs (each an SM, a key tile fetched once for 256 queries) in whole waves of the SMs; what is
+  // left, split into 128-row tiles, in clusters as large as the SMs and the key tiles allow. A rest
+  // whose tiles would not fit one wave goes paired too: two waves of half the length each.
   const int sms = device_sm_count();
-  const int64_t pairs = (int64_t)((L.T + kMaxRows - 1) / kMaxRows) * bh, tiles = (int64_t)((L.T + kRows - 1) / kRows) * bh;
-  const bool split = pairs < sms;
+  const int64_t per_row = (L.T + kMaxRows - 1) / kMaxRows;  // pairs of a (sequence, head)
+  const int64_t pairs = per_row * bh, over = pairs % sms;
+  // 128-row tiles of the last `over` pairs: a chunk of an odd number of them leaves one a row out
+  const int64_t over_tiles = 2 * over - ((L.T + kRows - 1) / kRows % 2 ? bh - (pairs - over) / per_row : 0);
+  const int64_t whole = over_tiles > sms ? pairs : pairs - over, rest = pairs - whole;
   const int64_t keys = (L.cap + kRows - 1) / kRows + (L.n + kRows - 1) / kRows;  // at most, for a query tile
-  a.cluster = 1;
-  while (split && a.cluster < kMaxCluster && tiles * a.cluster * 2 <= sms && keys >= 4 * a.cluster) a.cluster *= 2;
   const bool cap = L.softcap > 0.f, bias = L.slopes != nullptr;
-  auto kernel = split ? (cap ? (bias ? scored_prefill_kernel<true, true, true> : scored_prefill_kernel<true, false, true>)
-                             : (bias ? scored_prefill_kernel<false, true, true> : scored_prefill_kernel<false, false, true>))
-                      : (cap ? (bias ? scored_prefill_kernel<true, true, false> : scored_prefill_kernel<true, false, false>)
-                             : (bias ? scored_prefill_kernel<false, true, false> : scored_prefill_kernel<false, false, false>));
   static unsigned long long done[8] = {}, checked[8] = {};
-  const int which = 4 * split + 2 * cap + bias;
-  const size_t smem = sizeof(Smem);
-  if ((e = ensure_smem_limit(kernel, smem, &done[which])) != cudaSuccess) return e;
-  if (!__atomic_load_n(&checked[which], __ATOMIC_ACQUIRE)) {  // the register split draws on the launch's
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
-    if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidDeviceFunction;
-    __atomic_store_n(&checked[which], 1ull, __ATOMIC_RELEASE);
+  for (int split = 0; split < 2; ++split) {
+    const int64_t units = split ? 2 * rest : whole;
+    if (units == 0) continue;
+    a.first = split ? (int)whole : 0;
+    a.late = split && whole > 0 && pdl_enabled();
+    a.cluster = 1;
+    while (split && a.cluster < kMaxCluster && over_tiles * a.cluster * 2 <= sms && keys >= 4 * a.cluster) a.cluster *= 2;
+    auto kernel = split ? (cap ? (bias ? scored_prefill_kernel<true, true, true> : scored_prefill_kernel<true, false, true>)
+                               : (bias ? scored_prefill_kernel<false, true, true> : scored_prefill_kernel<false, false, true>))
+                        : (cap ? (bias ? scored_prefill_kernel<true, true, false> : scored_prefill_kernel<true, false, false>)
+                               : (bias ? scored_prefill_kernel<false, true, false> : scored_prefill_kernel<false, false, false>));
+    const int which = 4 * split + 2 * cap + bias;
+    const size_t smem = sizeof(Smem);
+    if ((e = ensure_smem_limit(kernel, smem, &done[which])) != cudaSuccess) return e;
+    if (!__atomic_load_n(&checked[which], __ATOMIC_ACQUIRE)) {  // the register split draws on the launch's
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+      if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+      __atomic_store_n(&checked[which], 1ull, __ATOMIC_RELEASE);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    fill_launch_config(cfg, attr, dim3((unsigned)(units * a.cluster)), dim3(kThreads), smem, stream);
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = a.cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, a, tq, tko, tvo, tpk, tpv, trk, trv)) != cudaSuccess) return e;
   }
-  const dim3 grid(split ? (L.T + kRows - 1) / kRows * a.cluster : (L.T + kMaxRows - 1) / kMaxRows, L.H, L.B);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  fill_launch_config(cfg, attr, grid, dim3(kThreads), smem, stream);
-  attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-  attr[cfg.numAttrs].val.clusterDim.x = a.cluster;
-  attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
-  ++cfg.numAttrs;
-  if ((e = cudaLaunchKernelEx(&cfg, kernel, a, tq, tko, tvo, tpk, tpv, trk, trv)) != cudaSuccess) return e;
   if (!L.write_ring) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
   fill_launch_config(cfg, attr, dim3(L.H, L.B), dim3(256), 0, stream);
   if ((e = cudaLaunchKernelEx(&cfg, ring_rows_kernel, L.H, L.n, L.T, static_cast<const uint4*>(L.k_out),
                               static_cast<const uint4*>(L.v_out), static_cast<uint4*>(L.ring_k_w),

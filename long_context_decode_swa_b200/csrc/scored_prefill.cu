@@ -12,9 +12,8 @@
 //     cluster of up to 8 CTAs deals the key tiles out among its CTAs; the parts meet through shared
 //     memory, the CTAs' through distributed shared memory.
 // While one stream's softmax runs, the tensor core works on the other's products. Roles: warp 0 TMA
-// producer of Q and K, warp 2 of V, warp 3 cleans V, one thread of warp 1 issues the MMAs, warps 4-7 / 8-11
-// softmax of stream A / B, thread r owning row r: its 128 scores are read from TMEM once and stay in registers (the softmax warps take
-// the registers that the others give up), and P (bf16) goes back over S as the A operand of P V.
+// producer of Q and K, warp 2 of V, warp 3 cleans V, one thread of warp 1 issues the MMAs, warps 4-11 /
+// 12-19 softmax of stream A / B, two threads a row; P (bf16) goes back over S as the A operand of P V.
 //
 // Documents: the union of the rows' ranges, as up to four runs of rows, gives the prefix tiles;
 // rows of a tile that no query of the CTA sees are zeroed in V (0 * NaN would reach O). A chunk over
@@ -22,7 +21,7 @@
 //
 // Scores: the special-function unit (16 a cycle and SM) bounds the kernel: one ex2 a score is 1,024
 // cycles a tile against 512 of MMA. tanh(u) = 1 - 2 / (e^2u + 1) would cost two more; where a warp's
-// scores all have |u| = |scale q.k| / cap <= 0.6 (or 1), tanh is u times a minimax polynomial in u^2
+// scores all have |u| = |scale q.k| / cap <= 0.4 (or 1), tanh is u times a minimax polynomial in u^2
 // instead, on the packed FMA pipe (errors below 1e-7 of the cap either way).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -46,13 +45,10 @@ constexpr int kRegionBytes = kRows * 128;  // one 64-column SW128 region of a 12
 constexpr int kTileBytes = 2 * kRegionBytes;
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
-constexpr int kThreads = 384;
-constexpr int kSoftmaxWarp0 = 4;
+constexpr int kThreads = 640;
+constexpr int kSoftmaxWarp0 = 4;           // warps 4-11: stream A, 12-19: stream B
+constexpr int kHalf = kRows / 2;           // key columns of a softmax thread
 constexpr int kMaxCluster = 8;
-// Registers a thread after the split: the block is launched with kLaunchRegs each (checked by
-// launch_scored_prefill), and the two shares must fit that.
-constexpr int kLaunchRegs = 168, kControlRegs = 80, kSoftmaxRegs = 208;
-static_assert(128 * kControlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kPartStride = kHeadDim + 4;  // floats of a row's part in shared memory (keeps rows off one bank)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
@@ -84,8 +80,13 @@ struct __align__(1024) Smem {
   int abort_flag;
   int seen_by[kKStages];  // with a key tile: the streams that see it, as bits
   Ctx ctx;
-  float stat_m[2][kRows];  // split: the streams' maxima,
-  float stat_l[2][kRows];  // and sums; [0] then holds the CTA's
+  float half[2][2][kRows];  // what the two halves of a stream's columns tell each other
+};
+static_assert(sizeof(Smem) <= 227 * 1024, "shared memory");
+
+// Split: a row's values on their way to the cluster, over the query tile that a split CTA does not have.
+struct RowStats {
+  float m[kRows], l[kRows], lse_ref[kRows];
 };
 static_assert((kKStages + kVStages) * kTileBytes >= kRows * kPartStride * 4, "parts lie over the K / V stages");
 
@@ -164,14 +165,6 @@ __device__ __forceinline__ bool wait_or_abort(Smem& sm, uint64_t* bar, uint32_t 
   sm.abort_flag = 1;
   set_status(status, RSWA_DEVICE_WAIT_TIMEOUT);
   return false;
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
 }
 
 __device__ __forceinline__ float min3(float a, float b, float c) {
@@ -387,8 +380,22 @@ __device__ __forceinline__ uint4 to_bf16x8(const float* o) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Both softmax groups meet.
-__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+// The 256 threads of a stream meet (barrier 1 + x); whether any of them says so.
+__device__ __forceinline__ bool stream_any(int x, bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(v ? 1u : 0u), "r"(1 + x)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void stream_barrier(int x) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + x) : "memory"); }
+// Both streams meet.
+__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 3, 512;" ::: "memory"); }
 
 template <bool kCap, bool kBias, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int x = 0; x < kQTiles; ++x) {
       mbar_init(&sm.s_full[x], 1);
-      mbar_init(&sm.p_full[x], 128);
+      mbar_init(&sm.p_full[x], 256);
       mbar_init(&sm.o_done[x], 1);
     }
     mbar_init(&sm.drain, 1);
@@ -558,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this CTA's t-th key tile
   auto tile_of = [&](int t, int& kind, int& start) { tile_kind(c, kSplit ? t * cluster + rank : t, kind, start); };
   if (warp < kSoftmaxWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     if (warp == 0 || warp == 2) {
       // ---------------- producers: Q and K tiles (warp 0), V tiles (warp 2) ----------------
       if (lane == 0) {
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t v = v_desc + (uint64_t)(vs * (kTileBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts(tmem + kColO + (uint32_t)x * 128u, tmem + (uint32_t)x * 128u + (uint32_t)kk * 8u,
+            tc_mma_ts(tmem + kColO + (uint32_t)x * 128u, tmem + (uint32_t)x * 128u + (uint32_t)((kk >> 2) * kHalf + (kk & 3) * 8),
                       v + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (more || kk > 0) ? 1u : 0u);
           tc_commit(&sm.o_done[x]);
         };
@@ -753,16 +759,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
   } else {
-    // (the two sides share no code after the split of the registers)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    // ---------------- softmax: thread r owns row r of its stream's tile ----------------
-    const int x = (warp - kSoftmaxWarp0) / 4;
-    const int r = tid - (kSoftmaxWarp0 + 4 * x) * 32;
+    // ---------------- softmax: two threads a row of a stream's tile, 64 key columns each ----------------
+    const int sw = warp - kSoftmaxWarp0;
+    const int x = sw >> 3, half = sw >> 2 & 1;
+    const int r = (sw & 3) * 32 + lane;
     const int row = (kSplit ? 0 : x * kRows) + r;  // row of the CTA
     const int i = c.i0 + row;
-    const uint32_t lane_base = (uint32_t)(((warp - kSoftmaxWarp0) & 3) * 32) << 16;
-    const uint32_t s_cols = tmem + lane_base + (uint32_t)x * 128u;
-    const uint32_t o_cols = tmem + lane_base + kColO;  // O of stream A; B's is 128 columns on
+    const int col0 = half * kHalf;
+    const uint32_t lane_base = (uint32_t)((sw & 3) * 32) << 16;
+    const uint32_t s_cols = tmem + lane_base + (uint32_t)(x * 128 + col0);  // its scores; its P goes over their first half
+    const uint32_t o_cols = tmem + lane_base + kColO;                       // O of stream A; B's is 128 columns on
     const int2 range = range_of(a, c.m, b, i, false);
     const float mul = kCap ? a.scale / a.softcap : a.scale * kLog2e;
     const float cap2 = a.softcap * kLog2e;
@@ -781,32 +787,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // l sums the unrounded weights, for O and lse alike: where one key dominates, O is off by the
     // rounding of its weight (at most half a bf16 step, as the output's own rounding); summing the
     // rounded ones too cost three more instructions a score pair
-    float m_used = -INFINITY, l = 0.f;
-    int j = 0;  // key tiles this stream has seen
+    float m_used = -INFINITY, l = 0.f;  // m_used is the same in both threads of a row
+    int j = 0;                          // key tiles this stream has seen
     bool ok = true;
     for (int t = kSplit ? x : 0; t < total; t += kSplit ? 2 : 1) {
       int kind, start;
       tile_of(t, kind, start);
       if (!kSplit && !tile_visible(c, x, kind, start)) continue;
       ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], j & 1, a.status));
-      if (!ok) break;
       tc_fence_after();
       const RowTile rt = row_tile(c, kind, start, i, range, pos, ref);
-      if (__all_sync(0xffffffffu, (rt.hi <= 0 || rt.lo >= kRows || rt.hi <= rt.lo) && rt.hi2 <= rt.lo2)) {
-        // no row of this warp sees a key of the tile
-        const uint32_t zero[16] = {};
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) tmem_st16(s_cols + (uint32_t)ch * 16u, zero);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&sm.p_full[x]);
-        ++j;
-        continue;
-      }
-      // The passes over the row's 128 scores go 32 columns at a time, through TMEM, in loops that are
-      // not unrolled: holding all 128 in registers made straight-line code of 20 to 40 KB a tile, which
-      // the instruction cache did not feed (a biased tile took 8,000 cycles instead of 2,000).
-      const bool full = __all_sync(0xffffffffu, rt.lo <= 0 && rt.hi >= kRows);
+      // does any row of this warp see one of its columns; do all rows see all of them
+      const int from = max(rt.lo, col0), from2 = max(rt.lo2, col0), to = col0 + kHalf;
+      const bool none = __all_sync(0xffffffffu, from >= min(rt.hi, to) && from2 >= min(rt.hi2, to));
+      const bool full = __all_sync(0xffffffffu, rt.lo <= col0 && rt.hi >= to);
+      // The passes over the row's scores go 32 columns at a time, through TMEM, in loops that are not
+      // unrolled: holding all of them in registers made straight-line code of 20 to 40 KB a tile, which
+      // the instruction cache did not feed (a biased tile took 8,000 cycles instead of 4,000).
       auto load = [&](int ch, float(&v)[32]) {
         uint32_t raw[32];
         tmem_ld32(s_cols + (uint32_t)ch * 32u, raw);
@@ -815,88 +812,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
       };
       Tanh how = kExact;
-      float lowest = INFINITY, highest = -INFINITY;
-      if (!kBias && full) {
+      bool fused = false;
+      float tmax = -INFINITY;
+      if (ok && !none) {
+        if (!kBias && full) {
+          float lowest = INFINITY, highest = -INFINITY;
 #pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          float v[32];
-          load(ch, v);
-          highest = highest_of(v, highest);
-          if (kCap) lowest = lowest_of(v, lowest);
-        }
-        if (kCap) how = tanh_of(lowest, highest, mul);
-      }
-      // without a mask or a bias the raw maximum is the maximum, and the scoring joins the exponentials' loop
-      const bool fused = !kBias && full && (!kCap || how != kExact);
-      float tmax;
-      if (fused) {
-        tmax = kCap ? cap2 * tanhf(highest * mul) : highest * mul;
-      } else {
-        tmax = -INFINITY;
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          float v[32];
-          load(ch, v);
-          score_chunk<kCap, kBias>(v, rt, ch * 32, full, mul, cap2, slope2, c.n);
-          tmax = highest_of(v, tmax);
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e]);
-          tmem_st32(s_cols + (uint32_t)ch * 32u, w);
-        }
-        tmem_wait_st();
-      }
-      const bool rescale = tmax > m_used + kLazyRescaleLog2;
-      float alpha = 1.f;
-      if (rescale) {
-        alpha = ex2(m_used - tmax);
-        l *= alpha;
-        m_used = tmax;
-      }
-      // the previous P V of this stream is done (the commit that completed S covers it)
-      if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-        for (int ch = 0; ch < 8; ++ch) {
-          uint32_t rr[16];
-          tmem_ld16(o_cols + (uint32_t)(x * 128 + ch * 16), rr);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
-          tmem_st16(o_cols + (uint32_t)(x * 128 + ch * 16), rr);
-        }
-      }
-      const float m_sub = m_used == -INFINITY ? 0.f : m_used;
-      float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-      auto weights = [&](auto&& less_m) {  // less_m: a pair of s -> score - m
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          float v[32];
-          load(ch, v);
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 z2 = less_m(make_float2(v[2 * e], v[2 * e + 1]));
-            const float2 p2 = make_float2(ex2(z2.x), ex2(z2.y));
-            const __nv_bfloat162 pb = __floats2bfloat162_rn(p2.x, p2.y);
-            pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
-            if (e & 1)
-              sum1 = __fadd2_rn(sum1, p2);
-            else
-              sum0 = __fadd2_rn(sum0, p2);
+          for (int ch = 0; ch < 2; ++ch) {
+            float v[32];
+            load(ch, v);
+            highest = highest_of(v, highest);
+            if (kCap) lowest = lowest_of(v, lowest);
           }
-          tmem_st16(s_cols + (uint32_t)ch * 16u, pk);
+          if (kCap) how = tanh_of(lowest, highest, mul);
+          // without a mask or a bias the raw maximum is the maximum, and the scoring joins the exponentials' loop
+          fused = !kCap || how != kExact;
+          tmax = kCap ? cap2 * tanhf(highest * mul) : highest * mul;
         }
-      };
-      const float2 minus_m = splat(-m_sub);
-      if (!fused)
-        weights([&](float2 z) { return __fadd2_rn(z, minus_m); });
-      else if (!kCap)
-        weights([&](float2 z) { return __ffma2_rn(z, splat(mul), minus_m); });
-      else if (how == kSmall)
-        weights([&](float2 z) { return capped_pair<TanhSmall>(z, mul, cap2, minus_m); });
-      else
-        weights([&](float2 z) { return capped_pair<TanhMid>(z, mul, cap2, minus_m); });
-      l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        if (!fused) {
+          tmax = -INFINITY;
+#pragma unroll 1
+          for (int ch = 0; ch < 2; ++ch) {
+            float v[32];
+            load(ch, v);
+            score_chunk<kCap, kBias>(v, rt, col0 + ch * 32, full, mul, cap2, slope2, c.n);
+            tmax = highest_of(v, tmax);
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e]);
+            tmem_st32(s_cols + (uint32_t)ch * 32u, w);
+          }
+          tmem_wait_st();
+        }
+      }
+      // Both halves of the stream meet here, also after a give-up. The running maximum only moves when
+      // it grows by more than 2^8 (the exponentials stay below 256): then the halves agree on it.
+      if (stream_any(x, !ok || tmax > m_used + kLazyRescaleLog2)) {
+        sm.half[x][half][r] = tmax;
+        if (stream_any(x, !ok)) {
+          ok = false;
+          break;
+        }
+        tmax = fmaxf(tmax, sm.half[x][half ^ 1][r]);
+        const bool rescale = tmax > m_used + kLazyRescaleLog2;
+        float alpha = 1.f;
+        if (rescale) {
+          alpha = ex2(m_used - tmax);
+          l *= alpha;
+          m_used = tmax;
+        }
+        // the previous P V of this stream is done (the commit that completed S covers it)
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t rr[32];
+            tmem_ld32(o_cols + (uint32_t)(x * 128 + col0 + ch * 32), rr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+            tmem_st32(o_cols + (uint32_t)(x * 128 + col0 + ch * 32), rr);
+          }
+        }
+      }
+      if (none) {
+        const uint32_t zero[16] = {};
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) tmem_st16(s_cols + (uint32_t)ch * 16u, zero);
+      } else {
+        const float2 minus_m = splat(m_used == -INFINITY ? 0.f : -m_used);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        auto weights = [&](auto&& less_m) {  // less_m: a pair of s -> score - m
+#pragma unroll 1
+          for (int ch = 0; ch < 2; ++ch) {
+            float v[32];
+            load(ch, v);
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 z2 = less_m(make_float2(v[2 * e], v[2 * e + 1]));
+              const float2 p2 = make_float2(ex2(z2.x), ex2(z2.y));
+              const __nv_bfloat162 pb = __floats2bfloat162_rn(p2.x, p2.y);
+              pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
+              if (e & 1)
+                sum1 = __fadd2_rn(sum1, p2);
+              else
+                sum0 = __fadd2_rn(sum0, p2);
+            }
+            tmem_st16(s_cols + (uint32_t)ch * 16u, pk);
+          }
+        };
+        if (!fused)
+          weights([&](float2 z) { return __fadd2_rn(z, minus_m); });
+        else if (!kCap)
+          weights([&](float2 z) { return __ffma2_rn(z, splat(mul), minus_m); });
+        else if (how == kSmall)
+          weights([&](float2 z) { return capped_pair<TanhSmall>(z, mul, cap2, minus_m); });
+        else
+          weights([&](float2 z) { return capped_pair<TanhMid>(z, mul, cap2, minus_m); });
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sm.p_full[x]);
@@ -904,15 +918,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && j > 0) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (j - 1) & 1, a.status));
     const float lse_ref = kBias ? slope2 * (float)ref : 0.f;
+    sm.half[x][half][r] = l;
     if (!kSplit) {
+      stream_barrier(x);  // all 256 threads of the stream come here, also after a give-up
       if (ok && j > 0) {
         tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum stays one)
-        uint4* orow = reinterpret_cast<uint4*>(a.out + (bh * a.T + i) * kHeadDim);
+        const float L = sm.half[x][0][r] + sm.half[x][1][r];
+        const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN sum stays one)
+        uint4* orow = reinterpret_cast<uint4*>(a.out + (bh * a.T + i) * kHeadDim + col0);
 #pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
+        for (int ch = 0; ch < 2; ++ch) {
           uint32_t rr[32];
-          tmem_ld32(o_cols + (uint32_t)(x * 128 + ch * 32), rr);
+          tmem_ld32(o_cols + (uint32_t)(x * 128 + col0 + ch * 32), rr);
           tmem_wait_ld();
           if (i < c.T) {
             float o[32];
@@ -922,34 +939,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) orow[ch * 4 + e] = to_bf16x8(o + 8 * e);
           }
         }
-        if (i < c.T && a.lse) a.lse[bh * a.T + i] = l == 0.f ? -INFINITY : (m_used + log2f(l) - lse_ref) * kLn2;
+        if (half == 0 && i < c.T && a.lse)
+          a.lse[bh * a.T + i] = L == 0.f ? -INFINITY : (m_used + log2f(L) - lse_ref) * kLn2;
       }
     } else {
-      // ---- the two streams' parts of the row meet; each group takes half of the columns ----
-      sm.stat_m[x][r] = m_used;
-      sm.stat_l[x][r] = l;
+      // ---- the two streams' parts of the row meet; each of the four groups takes 32 columns ----
+      RowStats* own = reinterpret_cast<RowStats*>(sm.q[1]);
+      if (half == 0) own[x].m[r] = m_used;
       tc_fence_before();
-      softmax_barrier();  // all 256 threads come here, also after a give-up
+      softmax_barrier();  // all 512 threads come here, also after a give-up
       tc_fence_after();
-      const float ma = sm.stat_m[0][r], mb = sm.stat_m[1][r];
+      const float ma = own[0].m[r], mb = own[1].m[r];
       const float M = fmaxf(ma, mb), m_sub = M == -INFINITY ? 0.f : M;
-      const bool none = total < 1, one = total < 2;  // streams without a key tile have no O
-      const float fa = none ? 0.f : ex2(ma - m_sub), fb = one ? 0.f : ex2(mb - m_sub);
-      const float L = fmaf(sm.stat_l[1][r], fb, sm.stat_l[0][r] * fa);
+      const bool empty = total < 1, one = total < 2;  // streams without a key tile have no O
+      const float fa = empty ? 0.f : ex2(ma - m_sub), fb = one ? 0.f : ex2(mb - m_sub);
+      const float L = fmaf(sm.half[1][0][r] + sm.half[1][1][r], fb, (sm.half[0][0][r] + sm.half[0][1][r]) * fa);
       const float inv = cluster > 1 ? 1.f : (L == 0.f ? 0.f : 1.f / L);
       float* part = reinterpret_cast<float*>(sm.k[0]) + r * kPartStride;  // every copy and MMA of the CTA is done
-      uint4* orow = reinterpret_cast<uint4*>(a.out + (bh * a.T + i) * kHeadDim);
-#pragma unroll 1
-      for (int ch = 0; ch < 2; ++ch) {
-        const int col = x * 64 + ch * 32;
+      {
+        const int col = (2 * x + half) * 32;
         uint32_t ra[32], rb[32];
-        if (!none) tmem_ld32(o_cols + (uint32_t)col, ra);
+        if (!empty) tmem_ld32(o_cols + (uint32_t)col, ra);
         if (!one) tmem_ld32(o_cols + 128u + (uint32_t)col, rb);
         tmem_wait_ld();
         float o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          o[e] = none ? 0.f : __uint_as_float(ra[e]) * fa;
+          o[e] = empty ? 0.f : __uint_as_float(ra[e]) * fa;
           if (!one) o[e] = fmaf(__uint_as_float(rb[e]), fb, o[e]);
           o[e] *= inv;
         }
@@ -958,29 +974,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(part + col + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         } else if (i < c.T) {
+          uint4* orow = reinterpret_cast<uint4*>(a.out + (bh * a.T + i) * kHeadDim + col);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) orow[col / 8 + e] = to_bf16x8(o + 8 * e);
+          for (int e = 0; e < 4; ++e) orow[e] = to_bf16x8(o + 8 * e);
         }
       }
       if (cluster == 1) {
-        if (x == 0 && i < c.T && a.lse) a.lse[bh * a.T + i] = L == 0.f ? -INFINITY : (M + log2f(L) - lse_ref) * kLn2;
+        if (x == 0 && half == 0 && i < c.T && a.lse)
+          a.lse[bh * a.T + i] = L == 0.f ? -INFINITY : (M + log2f(L) - lse_ref) * kLn2;
       } else {
-        softmax_barrier();  // both groups have read the streams' values
-        if (x == 0) {
-          sm.stat_m[0][r] = M;
-          sm.stat_l[0][r] = L;
-          sm.stat_l[1][r] = lse_ref;
+        RowStats& all = own[2];
+        if (x == 0 && half == 0) {
+          all.m[r] = M;
+          all.l[r] = L;
+          all.lse_ref[r] = lse_ref;
         }
         // ---- the cluster's parts meet: CTA `rank` joins rows [rank, rank + 1) * 128 / cluster ----
         cluster_sync();  // every CTA of the cluster comes here, also after a give-up
         const int rows = kRows / cluster;
-        for (int v = tid - kSoftmaxWarp0 * 32; v < rows * (kHeadDim / 8); v += 256) {
+        for (int v = tid - kSoftmaxWarp0 * 32; v < rows * (kHeadDim / 8); v += kThreads - kSoftmaxWarp0 * 32) {
           const int r2 = rank * rows + v / (kHeadDim / 8), d = v % (kHeadDim / 8) * 8, i2 = c.i0 + r2;
           if (i2 >= c.T) continue;
           float ms[kMaxCluster], Mc = -INFINITY;
 #pragma unroll
           for (int u = 0; u < kMaxCluster; ++u) {
-            ms[u] = u < cluster ? peer_f32(peer_smem(&sm.stat_m[0][r2], u)) : -INFINITY;
+            ms[u] = u < cluster ? peer_f32(peer_smem(&all.m[r2], u)) : -INFINITY;
             Mc = fmaxf(Mc, ms[u]);
           }
           const float mc_sub = Mc == -INFINITY ? 0.f : Mc;
@@ -989,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < kMaxCluster; ++u) {
             if (u >= cluster) break;
             const float f = exp2f(ms[u] - mc_sub);
-            Lc = fmaf(peer_f32(peer_smem(&sm.stat_l[0][r2], u)), f, Lc);
+            Lc = fmaf(peer_f32(peer_smem(&all.l[r2], u)), f, Lc);
             const uint32_t at = peer_smem(reinterpret_cast<const float*>(sm.k[0]) + r2 * kPartStride + d, u);
             const float4 p = peer_f32x4(at), q = peer_f32x4(at + 16);
             o[0] = fmaf(p.x, f, o[0]), o[1] = fmaf(p.y, f, o[1]), o[2] = fmaf(p.z, f, o[2]), o[3] = fmaf(p.w, f, o[3]);
@@ -1000,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 8; ++e) o[e] *= inv_c;
           reinterpret_cast<uint4*>(a.out + (bh * a.T + i2) * kHeadDim)[d / 8] = to_bf16x8(o);
           if (d == 0 && a.lse)
-            a.lse[bh * a.T + i2] = Lc == 0.f ? -INFINITY : (Mc + log2f(Lc) - sm.stat_l[1][r2]) * kLn2;
+            a.lse[bh * a.T + i2] = Lc == 0.f ? -INFINITY : (Mc + log2f(Lc) - all.lse_ref[r2]) * kLn2;
         }
         __syncwarp();
         cluster_sync();  // no CTA's shared memory goes away while another reads it
@@ -1088,7 +1106,7 @@ cudaError_t launch_scored_prefill(const ScoredPrefillLaunch& L, cudaStream_t str
   const int64_t whole = over_tiles > sms ? pairs : pairs - over, rest = pairs - whole;
   const int64_t keys = (L.cap + kRows - 1) / kRows + (L.n + kRows - 1) / kRows;  // at most, for a query tile
   const bool cap = L.softcap > 0.f, bias = L.slopes != nullptr;
-  static unsigned long long done[8] = {}, checked[8] = {};
+  static unsigned long long done[8] = {};
   for (int split = 0; split < 2; ++split) {
     const int64_t units = split ? 2 * rest : whole;
     if (units == 0) continue;
@@ -1103,12 +1121,6 @@ cudaError_t launch_scored_prefill(const ScoredPrefillLaunch& L, cudaStream_t str
     const int which = 4 * split + 2 * cap + bias;
     const size_t smem = sizeof(Smem);
     if ((e = ensure_smem_limit(kernel, smem, &done[which])) != cudaSuccess) return e;
-    if (!__atomic_load_n(&checked[which], __ATOMIC_ACQUIRE)) {  // the register split draws on the launch's
-      cudaFuncAttributes fa;
-      if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
-      if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidDeviceFunction;
-      __atomic_store_n(&checked[which], 1ull, __ATOMIC_RELEASE);
-    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     fill_launch_config(cfg, attr, dim3((unsigned)(units * a.cluster)), dim3(kThreads), smem, stream);

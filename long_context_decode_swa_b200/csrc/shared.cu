@@ -13,7 +13,9 @@
 // CTAs, so few long prefixes fill the chip as well as many short ones. A CTA walks its run in
 // segments, one per (tile, head), with roles as in the chunked prefill:
 //   warp 0 / warp 2, lane 0 : TMA producers of the K / V tiles, running ahead across segments
-//   warp 1                  : issues the MMAs; zeroes V rows past the prefix's end (0 * NaN)
+//   warp 1, one thread      : issues the MMAs, and nothing else (the tensor core's queue is shallow:
+//                             what it does between two MMAs is idle time)
+//   warp 3                  : zeroes V rows past the prefix's end (0 * NaN)
 //   warps 4-7, 8-11         : softmax groups A and B; thread r owns TMEM lane r of its group
 // With more than 128 sequences in the tile the groups take 128 rows each and read the same keys;
 // with fewer, both take the same rows and every other key tile, so that one group's exponentials
@@ -212,7 +214,7 @@ struct SharedSmem {
   uint8_t v[kVStages][kTileBytes];
   uint64_t q_full;
   uint64_t k_full[kKStages], k_empty[kKStages];
-  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t v_full[kVStages], v_ready[kVStages], v_empty[kVStages];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -281,6 +283,12 @@ struct Walk {
   __device__ __forceinline__ int events() const { return two() ? 2 * (k1 - k0) : k1 - k0; }
 };
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Both softmax groups meet; true for all of them if any thread gives up, so that they leave together.
 __device__ __forceinline__ bool softmax_barrier_or(bool stop) {
   uint32_t any;
@@ -314,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_ready[s], 1);
       mbar_init(&sm.v_empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -367,84 +376,132 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, n - stages); i < n; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer (lane 0), V-row zeroing (whole warp) ----------------
-    constexpr uint32_t kIdescQK = idesc_bf16_m128_n128(0);
-    constexpr uint32_t kIdescPV = idesc_bf16_m128_n128(1);
-    int base = 0;             // key tiles before this segment
-    uint32_t n_p[2] = {0, 0};  // P tiles consumed of each group
-    bool ok = true;
-    for (int seg = 0; ok && more; more = w.next(a.t, a.H), ++seg) {
-      const bool two = w.two();
-      const int events = w.events();
-      int k_seen = -1, v_seen = -1;  // tiles of this segment that were waited for
-      ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.q_full, seg & 1, a.status));
-      if (!ok) break;
-      tc_fence_after();
-      auto issue_s = [&](int e) {
-        const int x = e & 1, t = two ? e >> 1 : e, n = base + t, s = n % kKStages;
-        if (t > k_seen) {
-          if (!__all_sync(0xffffffffu, wait_or_abort(sm, &sm.k_full[s], (n / kKStages) & 1, a.status))) return false;
-          tc_fence_after();
-          k_seen = t;
-        }
-        if (lane == 0) {
-          const uint32_t q_addr = smem_addr(sm.q[two ? x : 0]);
-          const uint32_t k_addr = smem_addr(sm.k[s]);
+    // ---------------- MMA issuer: one thread ----------------
+    if (elect_one()) {
+      constexpr uint32_t kIdescQK = idesc_bf16_m128_n128(0);
+      constexpr uint32_t kIdescPV = idesc_bf16_m128_n128(1);
+      const uint64_t q_desc = smem_desc_sw128(smem_addr(sm.q[0]), 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_addr(sm.k[0]), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_addr(sm.v[0]), kRegionBytes, 1024);
+      int ks = 0, vs = 0;
+      uint32_t k_phase = 0, v_phase = 0, q_phase = 0, p_phase[2] = {0, 0};
+      auto issue_s = [&](int x, int q) {  // S_x = Q K^T, key tile in stage ks
+        const uint64_t qd = q_desc + (uint64_t)(q * (kTileBytes >> 4)), kd = k_desc + (uint64_t)(ks * (kTileBytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (uint32_t)(kk >> 2) * kRegionBytes + (uint32_t)(kk & 3) * 32u;
-            tc_mma_ss(tmem + (uint32_t)x * 128u, smem_desc_sw128(q_addr + off, 16, 1024),
-                      smem_desc_sw128(k_addr + off, 16, 1024), kIdescQK, kk > 0);
-          }
-          tc_commit(&sm.s_full[x]);
-          if (!two || x == 1) tc_commit(&sm.k_empty[s]);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * kRegionBytes + (kk & 3) * 32) >> 4);
+          tc_mma_ss(tmem + (uint32_t)x * 128u, qd + off, kd + off, kIdescQK, kk > 0);
         }
-        __syncwarp();
+        tc_commit(&sm.s_full[x]);
+      };
+      auto issue_pv = [&](int x, bool more_v) {  // O_x += P_x V, value tile in stage vs
+        const uint64_t vd = v_desc + (uint64_t)(vs * (kTileBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_ts(tmem + kColO + (uint32_t)x * 128u, tmem + (uint32_t)x * 128u + (uint32_t)kk * 8u,
+                    vd + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (more_v || kk > 0) ? 1u : 0u);
+        tc_commit(&sm.o_done[x]);
+      };
+      auto take_k = [&]() {
+        if (!wait_or_abort(sm, &sm.k_full[ks], k_phase, a.status)) return false;
+        tc_fence_after();
         return true;
       };
-      for (int e = 0; ok && e < min(2, events); ++e) ok = issue_s(e);
-      for (int e = 0; ok && e < events; ++e) {
-        const int x = e & 1, t = two ? e >> 1 : e, n = base + t, s = n % kVStages;
-        if (t > v_seen) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[s], (n / kVStages) & 1, a.status));
-          if (!ok) break;
-          v_seen = t;
-          const int left = w.t.len - (w.k0 + t) * kRows;  // rows of the prefix in this tile
-          if (left < kRows) {
-            for (int r = left + lane; r < kRows; r += 32) {
-              uint4* row0 = reinterpret_cast<uint4*>(sm.v[s] + r * 128);
-              uint4* row1 = reinterpret_cast<uint4*>(sm.v[s] + kRegionBytes + r * 128);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                row0[i] = make_uint4(0, 0, 0, 0);
-                row1[i] = make_uint4(0, 0, 0, 0);
-              }
+      auto free_k = [&]() {
+        tc_commit(&sm.k_empty[ks]);
+        if (++ks == kKStages) {
+          ks = 0;
+          k_phase ^= 1;
+        }
+      };
+      auto take_p = [&](int x) {
+        if (!wait_or_abort(sm, &sm.p_full[x], p_phase[x], a.status)) return false;
+        p_phase[x] ^= 1;
+        tc_fence_after();
+        return true;
+      };
+      bool ok = true;
+      for (; ok && more; more = w.next(a.t, a.H)) {
+        const int n = w.k1 - w.k0;
+        if (!(ok = wait_or_abort(sm, &sm.q_full, q_phase, a.status))) break;
+        q_phase ^= 1;
+        tc_fence_after();
+        if (w.two()) {
+          if ((ok = take_k())) {
+            issue_s(0, 0);
+            issue_s(1, 1);
+            free_k();
+          }
+        } else {
+          for (int t = 0; ok && t < min(2, n); ++t)
+            if ((ok = take_k())) {
+              issue_s(t, 0);
+              free_k();
             }
-            fence_async_smem();
-            __syncwarp();
+        }
+        for (int t = 0; ok && t < n; ++t) {
+          if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a.status))) break;
+          if (w.two()) {
+            const bool next = t + 1 < n;
+            if (!(ok = take_p(0))) break;
+            issue_pv(0, t > 0);
+            if (next) {
+              if (!(ok = take_k())) break;
+              issue_s(0, 0);
+            }
+            if (!(ok = take_p(1))) break;
+            issue_pv(1, t > 0);
+            tc_commit(&sm.v_empty[vs]);
+            if (next) {
+              issue_s(1, 1);
+              free_k();
+            }
+          } else {
+            const int x = t & 1;
+            if (!(ok = take_p(x))) break;
+            issue_pv(x, t > 1);
+            tc_commit(&sm.v_empty[vs]);
+            if (t + 2 < n) {
+              if (!(ok = take_k())) break;
+              issue_s(x, 0);
+              free_k();
+            }
+          }
+          if (++vs == kVStages) {
+            vs = 0;
+            v_phase ^= 1;
           }
         }
-        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.p_full[x], n_p[x] & 1, a.status));
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t v_addr = smem_addr(sm.v[s]);
-          const uint32_t p_tmem = tmem + (uint32_t)x * 128u;
-          const uint32_t o_tmem = tmem + kColO + (uint32_t)x * 128u;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts(o_tmem, p_tmem + (uint32_t)kk * 8u, smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, kRegionBytes, 1024),
-                      kIdescPV, (e > 1 || kk > 0) ? 1u : 0u);
-          tc_commit(&sm.o_done[x]);
-          if (!two || x == 1) tc_commit(&sm.v_empty[s]);
-        }
-        __syncwarp();
-        ++n_p[x];
-        if (e + 2 < events) ok = issue_s(e + 2);
       }
-      base += w.k1 - w.k0;
+      tc_commit(&sm.drain);  // fires once every issued MMA is done
     }
-    if (lane == 0) tc_commit(&sm.drain);  // fires once every issued MMA is done
+    __syncwarp();
+  } else if (warp == 3) {
+    // ---------------- V rows past the prefix's end: zeroed ----------------
+    int n = 0;
+    bool ok = true;
+    for (; ok && more; more = w.next(a.t, a.H)) {
+      for (int k = w.k0; ok && k < w.k1; ++k, ++n) {
+        const int s = n % kVStages;
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[s], (n / kVStages) & 1, a.status));
+        if (!ok) break;
+        const int left = w.t.len - k * kRows;  // rows of the prefix in this tile
+        if (left < kRows) {
+          for (int r = left + lane; r < kRows; r += 32) {
+            uint4* row0 = reinterpret_cast<uint4*>(sm.v[s] + r * 128);
+            uint4* row1 = reinterpret_cast<uint4*>(sm.v[s] + kRegionBytes + r * 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              row0[i] = make_uint4(0, 0, 0, 0);
+              row1[i] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&sm.v_ready[s]);
+      }
+    }
   } else if (warp >= kSoftmaxWarp0) {
     // ---------------- softmax groups ----------------
     const int x = (warp - kSoftmaxWarp0) / 4;

@@ -11,9 +11,11 @@
 // |pos| * 2^-65 + 2^-32 turns for every int32 position without fp64 arithmetic, whose rate
 // on this chip would bound the kernel (the page2d kernel's fp64 sincos is its second cost).
 //
-// HBM-bound: every element is read once and written once. A CTA takes a group of tokens and
-// all their heads, so that one table of cos / sin serves every head; a thread holds up to
-// four units (two 16-byte vectors each) in flight while the CTA fills the table.
+// HBM-bound: every element is read once and written once. A warp takes the rows of a few
+// consecutive tokens (four at 128 bf16 dims: 1 KiB runs) in up to 8 heads, four heads at a time in
+// flight; a lane keeps its place in the row, so that the cos and sin of its pairs stay in its registers
+// for all heads, with no table and no barrier (a CTA-wide table in shared memory, filled behind the loads
+// of 4 or 16 tokens, measured 77 to 90 us where this takes 42, as a plain copy does: the loads waited for it).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -24,8 +26,8 @@ namespace rswa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;       // units a thread holds per pass
-constexpr int kMaxGroup = 16;   // tokens per CTA
+constexpr int kBatch = 4;       // heads of a row in flight
+constexpr int kMaxHeads = 8;    // heads of a warp
 constexpr int kMaxPairs = 128;  // rot <= 256
 
 struct RowStrides {
@@ -38,7 +40,8 @@ struct Rope1dArgs {
   int units;     // D / (2 vectors): units of one row
   int rot_units; // of them rotated
   int half;      // rot / 2
-  int group;
+  int tokens;    // of a warp: 32 / units
+  int heads;     // of a warp
   int copy;      // the dims past rot have to be copied (not in place)
   const void* q;
   void* q_out;
@@ -87,7 +90,7 @@ struct Vec<float> {
 // Rotates the unit's two vectors: half layout: x's of N pairs, then their y's; interleaved:
 // N / 2 pairs in each vector. cs: the unit's N pairs.
 template <typename E, bool kInterleaved>
-__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2* cs) {
+__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2 (&cs)[Vec<E>::kN]) {
   constexpr int N = Vec<E>::kN;
   float x[N], y[N];
   Vec<E>::get(a, x);
@@ -116,70 +119,65 @@ __device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2* cs) {
 }
 
 template <typename E, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rope1d_kernel(const __grid_constant__ Rope1dArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rope1d_kernel(const __grid_constant__ Rope1dArgs a) {
   constexpr int N = Vec<E>::kN;
-  __shared__ float2 cs[kMaxGroup * kMaxPairs];
-  __shared__ int2 at[kMaxGroup];  // (sequence, token) of each row of the group
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t r0 = (int64_t)blockIdx.x * a.group;
-  const int g_rows = (int)min((int64_t)a.group, a.rows - r0);
-  if ((int)threadIdx.x < g_rows) {
-    const int64_t r = r0 + threadIdx.x;
-    const int b = (int)(r / a.T);
-    at[threadIdx.x] = make_int2(b, (int)(r - (int64_t)b * a.T));
-  }
-  __syncthreads();
-  const int per_head = g_rows * a.units;
-  const int total = per_head * a.H;
-  for (int u0 = 0; u0 < total; u0 += kUnits * kThreads) {
-    uint4 va[kUnits], vb[kUnits];
-    E* dst[kUnits];
-    int ci[kUnits];
+  const int lane = threadIdx.x & 31;
+  const int64_t group = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  // this lane's unit c of the rows of token r
+  const int g = lane / a.units, c = lane - g * a.units;
+  const int64_t r = group * a.tokens + g;
+  const bool turned = c < a.rot_units;
+  if (g >= a.tokens || r >= a.rows || !(turned || a.copy)) return;
+  const int first = (turned && !kInterleaved) ? c * N : 2 * c * N;
+  const int second = (turned && !kInterleaved) ? a.half : N;  // from the first vector to the second
+  const int pos = a.pos[r];
+  int64_t b;
+  if (a.rows <= 0x7fffffff)
+    b = (unsigned)r / (unsigned)a.T;
+  else
+    b = r / a.T;
+  const int64_t t = r - b * a.T;
+  const E* q = static_cast<const E*>(a.q) + b * a.qs.b + t * a.qs.t + first;
+  E* q_out = static_cast<E*>(a.q_out) + b * a.qos.b + t * a.qos.t + first;
+  const E* k = static_cast<const E*>(a.k) + b * a.ks.b + t * a.ks.t + first - a.Hq * a.ks.h;
+  E* k_out = static_cast<E*>(a.k_out) + b * a.kos.b + t * a.kos.t + first - a.Hq * a.kos.h;
+  const int h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.H);
+  float2 cs[N];
+  for (int hb = h0; hb < h1; hb += kBatch) {
+    uint4 va[kBatch], vb[kBatch];
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const int u = u0 + j * kThreads + (int)threadIdx.x;
-      dst[j] = nullptr;
-      ci[j] = 0;
-      if (u >= total) continue;
-      // consecutive threads walk a head's rows of consecutive tokens
-      const int h = u / per_head, rem = u - h * per_head;
-      const int g = rem / a.units, c = rem - g * a.units;
-      const bool turned = c < a.rot_units;
-      if (!turned && !a.copy) continue;
-      const int2 bt = at[g];
-      const bool is_q = h < a.Hq;
-      const int hh = is_q ? h : h - a.Hq;
-      const RowStrides& si = is_q ? a.qs : a.ks;
-      const RowStrides& so = is_q ? a.qos : a.kos;
-      const E* src = static_cast<const E*>(is_q ? a.q : a.k) + bt.x * si.b + hh * si.h + bt.y * si.t;
-      const int first = (turned && !kInterleaved) ? c * N : 2 * c * N;
-      const int second = (turned && !kInterleaved) ? a.half + c * N : first + N;
-      va[j] = *reinterpret_cast<const uint4*>(src + first);
-      vb[j] = *reinterpret_cast<const uint4*>(src + second);
-      dst[j] = static_cast<E*>(is_q ? a.q_out : a.k_out) + bt.x * so.b + hh * so.h + bt.y * so.t + first;
-      ci[j] = turned ? g * a.half + c * N : -1;
-    }
-    if (u0 == 0) {  // the group's cos / sin, while its loads are in flight
-      for (int p = threadIdx.x; p < g_rows * a.half; p += kThreads) {
-        const int g = p / a.half, i = p - g * a.half;
-        const uint64_t turn = (uint64_t)(int64_t)a.pos[r0 + g] * a.turns[i];
-        float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
-        cs[p] = make_float2(c * a.mscale, s * a.sign);
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = hb + j;
+      if (h < h1) {
+        const E* src = h < a.Hq ? q + h * a.qs.h : k + h * a.ks.h;
+        va[j] = *reinterpret_cast<const uint4*>(src);
+        vb[j] = *reinterpret_cast<const uint4*>(src + second);
       }
-      __syncthreads();
+    }
+    if (hb == h0 && turned) {  // this lane's cos / sin, while its loads are in flight
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint64_t turn = (uint64_t)(int64_t)pos * a.turns[c * N + i];
+        const float part = (float)(int32_t)(turn >> 32);  // of a turn, times 2^32: half a turn either way
+        float s, co;
+        if (sizeof(E) == 2)  // good to 2^-21.2 here, far below a bf16 step
+          __sincosf(part * 1.4629180792671596e-9f, &s, &co);  // 2 pi / 2^32
+        else
+          sincospif(part * 4.656612873077393e-10f, &s, &co);  // 2^-31
+        cs[i] = make_float2(co * a.mscale, s * a.sign);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      if (dst[j] == nullptr) continue;
-      int second = N;
-      if (ci[j] >= 0) {
-        rotate<E, kInterleaved>(va[j], vb[j], cs + ci[j]);
-        if (!kInterleaved) second = a.half;
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = hb + j;
+      if (h < h1) {
+        if (turned) rotate<E, kInterleaved>(va[j], vb[j], cs);
+        E* dst = h < a.Hq ? q_out + h * a.qos.h : k_out + h * a.kos.h;
+        *reinterpret_cast<uint4*>(dst) = va[j];
+        *reinterpret_cast<uint4*>(dst + second) = vb[j];
       }
-      *reinterpret_cast<uint4*>(dst[j]) = va[j];
-      *reinterpret_cast<uint4*>(dst[j] + second) = vb[j];
     }
   }
 }
@@ -210,20 +208,23 @@ cudaError_t launch_rope1d(const Rope1dLaunch& L, cudaStream_t stream) {
   a.mscale = L.mscale;
   a.sign = L.inverse ? -L.mscale : L.mscale;
   for (int i = 0; i < a.half; ++i) a.turns[i] = L.turns[i];
-  // tokens of a CTA: one pass of four units a thread where the rows are few enough
-  const int per_row = a.H * a.units;
-  int group = kUnits * kThreads / per_row;
-  group = group < 1 ? 1 : (group > kMaxGroup ? kMaxGroup : group);
-  // a call of few tokens is spread over the SMs instead
-  while (group > 1 && (a.rows + group - 1) / group < device_sm_count()) --group;
-  a.group = group;
-  const int64_t grid = (a.rows + group - 1) / group;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  a.tokens = 32 / a.units;
+  // few rows: fewer heads a warp and smaller CTAs, until every SM has one
+  const int sms = device_sm_count();
+  const int64_t groups = (a.rows + a.tokens - 1) / a.tokens;
+  a.heads = a.H < kMaxHeads ? a.H : kMaxHeads;
+  int warps = kThreads / 32;
+  auto ctas = [&]() { return (groups + warps - 1) / warps * ((a.H + a.heads - 1) / a.heads); };
+  while (a.heads > kBatch && ctas() < 4 * sms) a.heads = (a.heads + 1) / 2;
+  while (warps > 1 && ctas() < sms) warps /= 2;
+  while (a.heads > 1 && ctas() < sms) a.heads = (a.heads + 1) / 2;
+  if ((groups + warps - 1) / warps > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((groups + warps - 1) / warps), (a.H + a.heads - 1) / a.heads);
   auto kernel = L.f32 ? (L.interleaved ? rope1d_kernel<float, true> : rope1d_kernel<float, false>)
                       : (L.interleaved ? rope1d_kernel<uint16_t, true> : rope1d_kernel<uint16_t, false>);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  fill_launch_config(cfg, attr, dim3((unsigned)grid), dim3(kThreads), 0, stream);
+  fill_launch_config(cfg, attr, grid, dim3(warps * 32), 0, stream);
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 

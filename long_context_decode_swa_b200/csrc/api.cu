@@ -1125,6 +1125,9 @@ static rswa_status balanced_args(const char* fn, const rswa_dims* dims, const vo
   REQUIRE_PTR(out);
   REQUIRE_PTR(workspace);
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RSWA_ERR_INVALID, "%s: scale must be finite and > 0", fn);
+  const int64_t tiles = (dims->prefix_cap + rswa::kBlock - 1) / rswa::kBlock + (dims->ring + rswa::kBlock - 1) / rswa::kBlock + 1;
+  if ((int64_t)dims->batch * dims->heads * tiles > INT32_MAX)
+    return fail(RSWA_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of 32 rows", fn);
   *a = rswa::BalancedArgs{};
   a->B = dims->batch;
   a->H = dims->heads;
@@ -1282,6 +1285,9 @@ rswa_status rswa_decode_shared(const rswa_dims* dims, int32_t n_shared, int64_t 
     return fail(RSWA_ERR_INVALID, "%s: shared_cap out of range (got %lld)", fn, (long long)shared_cap);
   if ((int64_t)n_shared * dims->heads * shared_cap >= ((int64_t)1 << 31) - 1)
     return fail(RSWA_ERR_UNSUPPORTED, "%s: more than 2^31 shared rows", fn);
+  // every prefix can leave one group of 256 sequences part full
+  if ((n_shared + (int64_t)dims->batch / rswa::kSharedRows) * dims->heads * ((shared_cap + 127) / 128) > INT32_MAX)
+    return fail(RSWA_ERR_UNSUPPORTED, "%s: more than 2^31 (sequence group, head, key tile) units", fn);
   const size_t need = rswa_decode_shared_workspace_bytes(dims, n_shared);
   if (ws_bytes < need)
     return fail(RSWA_ERR_INVALID, "%s: workspace of %zu bytes is smaller than the %zu required", fn, ws_bytes, need);

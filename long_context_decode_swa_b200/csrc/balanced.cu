@@ -33,21 +33,10 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTileBytes = kBlock * kRowBytes;  // 8 KiB
 constexpr int kCtasPerSm = 2;                   // by shared memory
 constexpr int kSoloItems = 4;
+constexpr int kWholeItems = 3;
 constexpr int kWholeRounds = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-
-struct BalancedSmem {
-  uint8_t stage[kWarps][2][kTileBytes];
-  uint64_t full[kWarps];
-  float wm[kWarps], wl[kWarps], wlu[kWarps];
-  float wacc[kWarps][kHeadDim];
-  long long scan[kWarps];
-  int most[kWarps];
-  long long start_base[kWarps];  // units before the sequence that the team's share starts in
-  int start_b[kWarps];
-  int is_last;
-};
 
 // A sequence's rows: prefix rows [lo, hi) and the ring's valid slots in up to two runs.
 struct SeqRows {
@@ -56,6 +45,19 @@ struct SeqRows {
   int wp;
   int n_pre, n_r0;
   int tiles;  // >= 1: a sequence without rows still owns one (empty) unit, which writes its output
+};
+
+struct BalancedSmem {
+  uint8_t stage[kWarps][2][kTileBytes];
+  uint64_t full[kWarps];
+  float wm[kWarps], wl[kWarps], wlu[kWarps];
+  float wacc[kWarps][kHeadDim];
+  int scan[kWarps];
+  int most[kWarps];
+  SeqRows start_rows[kWarps];  // of the sequence that the team's share starts in,
+  int start_b[kWarps];
+  int start_base[kWarps];      // and the units before it
+  int is_last;
 };
 
 template <bool kScored>
@@ -296,30 +298,7 @@ __device__ __forceinline__ void join(State& s, const float* rec, int c) {
   s.acc[3] = make_float2(fmaf(s.acc[3].x, fs, r1.z * fr), fmaf(s.acc[3].y, fs, r1.w * fr));
 }
 
-// Where the shared part's records of a sequence lie: one a head for each CTA that had a run of its keys.
-struct SharedSeq {
-  int row;  // -1: none
-  int first_seq, rows, key_tiles;
-  long long first_unit, per;
-};
-
-__device__ __forceinline__ SharedSeq shared_seq(const BalancedArgs& a, int b) {
-  SharedSeq r;
-  r.row = -1;
-  r.first_seq = r.rows = r.key_tiles = 0;
-  r.first_unit = r.per = 1;
-  const int ti = a.shared.seq_tile[b];
-  if (ti < 0) return r;
-  const SharedTile t = a.shared.tiles[ti];
-  r.row = a.shared.seq_row[b];
-  r.first_seq = t.first_seq;
-  r.rows = t.rows;
-  r.key_tiles = t.key_tiles;
-  r.first_unit = t.first_unit;
-  r.per = a.shared.head->per;
-  return r;
-}
-
+// The records that the shared part left for (b, h): one for each CTA that had a run of its keys.
 struct SharedRecords {
   int count;
   const float* first;  // the run that holds the first key tile
@@ -329,13 +308,13 @@ struct SharedRecords {
   }
 };
 
-__device__ __forceinline__ SharedRecords shared_records(const BalancedArgs& a, const SharedSeq& t, int h) {
+__device__ __forceinline__ SharedRecords shared_records(const BalancedArgs& a, const SharedSeq& t, int per, int h) {
   SharedRecords r;
   r.count = 0;
   r.first = r.next = nullptr;
   if (t.row < 0) return r;
-  const long long u = t.first_unit + (long long)h * t.key_tiles;
-  const int c0 = (int)(u / t.per), c1 = (int)((u + t.key_tiles - 1) / t.per);
+  const int u = t.first_unit + h * t.key_tiles;
+  const int c0 = u / per, c1 = (u + t.key_tiles - 1) / per;
   r.count = c1 - c0 + 1;
   r.first = a.shared.records + ((int64_t)t.first_seq * a.H + (int64_t)h * t.rows + t.row) * kRecordFloats;
   r.next = a.shared.records + ((int64_t)a.B * a.H + (int64_t)(c0 + 1) * kSharedRows + t.row) * kRecordFloats;
@@ -352,24 +331,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
     for (int s = 0; s < kWarps; ++s) mbar_init(&sm.full[s], 1);
     fence_mbar_init();
   }
-  griddep_wait();
+  // With a shared part, its launch is the one before: its records are waited for where they are
+  // joined, and until then this launch runs beside it (on the SMs that it leaves free, or leaves).
+  // What came before the shared part has ended: this launch started after all CTAs of that one had
+  // waited for it.
+  if (!kShared) griddep_wait();
   griddep_launch_dependents();
 
-  // ---- this CTA's share of the line of units ----
+  // ---- this CTA's share of the line of units (fewer than 2^31, as the entry points see to) ----
   const int per_thread = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per_thread), b1 = min(a.B, b0 + per_thread);
-  long long mine = 0;
+  int mine = 0;
   int most = 0;  // tiles of the longest item
+  SeqRows rows0;  // of sequence b0
   for (int b = b0; b < b1; ++b) {
-    const int tiles = rows_of<kScored>(a, b, blockIdx.x == 0).tiles;
-    mine += tiles;
-    most = max(most, tiles);
+    const SeqRows r = rows_of<kScored>(a, b, blockIdx.x == 0);
+    if (b == b0) rows0 = r;
+    mine += r.tiles;
+    most = max(most, r.tiles);
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  long long inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+    const int t = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += t;
   }
   if (lane == 31) {
@@ -377,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
     sm.most[warp] = most;
   }
   __syncthreads();
-  long long before = inc - mine, total = 0;
+  int before = inc - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     before += w < warp ? sm.scan[w] : 0;
@@ -392,41 +377,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
   // where a CTA gets that many, and, where there are no more items than CTAs, one to a CTA as long
   // as it is done in a few rounds of the six warps (records to join cost more). Else shares cut
   // through items.
-  long long per = (total + gridDim.x - 1) / gridDim.x;
+  const int grid = gridDim.x;
+  int per = (total - 1) / grid + 1;
   Share share;
-  share.solo = per >= (long long)kSoloItems * kWarps * most;
-  share.whole = share.solo || per >= (long long)kSoloItems * most || (per <= most && most <= kWholeRounds * kWarps);
+  share.solo = per >= kSoloItems * kWarps * most;
+  share.whole = share.solo || per >= kWholeItems * most || (per <= most && most <= kWholeRounds * kWarps);
   if (share.solo)
-    per = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);
+    per = (total - 1) / (grid * kWarps) + 1;
   else
-    per = max(per, (long long)(share.whole ? most : kWarps));  // fewer units than warps: idle warps, more records
+    per = max(per, share.whole ? most : kWarps);  // fewer units than warps: idle warps, more records
   const int step = share.solo ? 1 : kWarps;
   const int slot = share.solo ? warp : 0;  // this warp's team in the CTA
-  const long long team0 = (long long)blockIdx.x * (share.solo ? kWarps : 1);
+  const int team0 = (int)blockIdx.x * (share.solo ? kWarps : 1);
   for (int w = 0; w < (share.solo ? kWarps : 1); ++w) {
-    const long long u = (team0 + w) * per;
-    if (mine > 0 && u >= before && u < before + mine) {
-      long long base = before;
-      int b = b0;
-      for (;; ++b) {
-        const long long units = (long long)rows_of<kScored>(a, b, false).tiles * a.H;
-        if (u < base + units) break;
-        base += units;
+    const int64_t u = (int64_t)(team0 + w) * per;
+    if (mine > 0 && u >= before && u < (int64_t)before + mine) {
+      int base = before, b = b0;
+      SeqRows r = rows0;
+      while (u >= base + r.tiles * a.H) {
+        base += r.tiles * a.H;
+        r = rows_of<kScored>(a, ++b, false);
       }
+      sm.start_rows[w] = r;
       sm.start_b[w] = b;
       sm.start_base[w] = base;
     }
   }
   __syncthreads();
-  const long long u0 = (team0 + slot) * per;
-  if (u0 >= total) return;  // a whole team: no barrier follows for it
-  share.units = (int)min(per, total - u0);
+  if ((int64_t)(team0 + slot) * per >= total) return;  // a whole team: no barrier follows for it
+  const int u0 = (team0 + slot) * per;
+  share.units = min(per, total - u0);
 
   Cursor ahead;  // where this warp issues copies
   ahead.b = sm.start_b[slot];
-  ahead.s = rows_of<kScored>(a, ahead.b, false);
-  ahead.h = (int)((u0 - sm.start_base[slot]) / ahead.s.tiles);
-  ahead.first = (int)(sm.start_base[slot] + (long long)ahead.h * ahead.s.tiles - u0);
+  ahead.s = sm.start_rows[slot];
+  ahead.h = (u0 - sm.start_base[slot]) / ahead.s.tiles;
+  ahead.first = sm.start_base[slot] + ahead.h * ahead.s.tiles - u0;
   if (share.whole && ahead.first < 0) {  // that item is another team's
     if (u0 + ahead.first + ahead.s.tiles >= total) return;
     advance<kScored>(a, ahead);
@@ -437,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
   u += share.solo ? 0 : warp;
   Tile tile = issue<kScored>(a, sm, u, share, ahead, warp, lane);
   SharedSeq seq;
-  int seq_b = -1;
+  int seq_b = -1, shared_per = 1;
   uint4 q_next = *reinterpret_cast<const uint4*>(a.q + ((int64_t)at.b * a.H + at.h) * kHeadDim + c * 8);
   uint32_t phase = 0;
   bool ok = true;
@@ -478,15 +464,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
     }
     if (bh + 1 < (int64_t)a.B * a.H)  // the next item's query, while this one streams
       q_next = *reinterpret_cast<const uint4*>(a.q + (bh + 1) * kHeadDim + c * 8);
-    SharedRecords sr;
-    sr.count = 0;
-    if (kShared) {
-      if (seq_b != at.b) {
-        seq = shared_seq(a, at.b);
-        seq_b = at.b;
-      }
-      sr = shared_records(a, seq, at.h);
-    }
     State st;
     clear(st);
     for (; ok && u < end; u += step) {
@@ -508,8 +485,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
     }
     fold(st);
     const bool starts = at.first >= 0, ends = share.whole || at.first + at.s.tiles <= share.units;
-    if (kShared && starts && ends)  // the whole item is here: the shared part's records join its warps
-      for (int r = share.solo ? 0 : warp; r < sr.count; r += step) join(st, sr.at(r), c);
+    SharedRecords sr;
+    sr.count = 0;
+    if (kShared) {
+      if (seq_b < 0) {  // the first item: the shared part has to be done now
+        griddep_wait();
+        shared_per = a.shared.head->per;
+      }
+      if (seq_b != at.b) {
+        seq = a.shared.seqs[at.b];
+        seq_b = at.b;
+      }
+      sr = shared_records(a, seq, shared_per, at.h);
+      if (starts && ends)  // the whole item is here: the shared part's records join its warps
+        for (int r = share.solo ? 0 : warp; r < sr.count; r += step) join(st, sr.at(r), c);
+    }
 
     if (share.solo) {
       if (g == 0 && ok) {
@@ -593,8 +583,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
       __threadfence();
       __syncthreads();
       // CTAs c0..c1 hold a part of this item; c0, where it starts, keeps its counter
-      const long long s0 = u0 + at.first, s1 = s0 + at.s.tiles - 1;
-      const int c0 = (int)(s0 / per), c1 = (int)(s1 / per);
+      const int s0 = u0 + at.first, c0 = s0 / per, c1 = (s0 + at.s.tiles - 1) / per;
       if (tid == 0) sm.is_last = atomicAdd(&a.counters[c0], 1) == c1 - c0;
       __syncthreads();
       if (!sm.is_last) break;

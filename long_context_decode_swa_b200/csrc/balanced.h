@@ -13,31 +13,36 @@ constexpr int kRecordFloats = 4 + 128;  // max, sum of the weights that met V, s
 constexpr int kSharedRows = 256;        // sequences that one pass over a shared prefix serves
 
 // Up to kSharedRows sequences over one shared prefix. Units of the shared part: key tiles of 128,
-// a tile's heads one after the other.
+// a tile's heads one after the other. (The entry point keeps the units of a call below 2^31.)
 struct SharedTile {
-  long long first_unit;
+  int first_unit;
   int first_seq;  // its sequences: order[first_seq .. first_seq + rows)
   int rows;
   int prefix;
   int len;        // rows of the prefix
   int key_tiles;
-  int pad;
+  int pad[2];
 };
 
-struct SharedHead {
-  long long units;  // of all tiles and heads
-  long long per;    // units a CTA takes: CTA c has [c per, (c + 1) per)
-  int tiles;
+// Where a sequence's shared part is: row `row` (-1: it has none) of a tile with these fields.
+struct SharedSeq {
+  int row, first_seq, rows, key_tiles, first_unit;
   int pad[3];
 };
 
+struct SharedHead {
+  int units;  // of all tiles and heads
+  int per;    // units a CTA takes: CTA c has [c per, (c + 1) per)
+  int tiles;
+  int pad;
+};
+
 struct SharedTables {
-  const SharedHead* head;     // null: no shared part
-  const SharedTile* tiles;
-  const int32_t* order;       // sequences, grouped by prefix
-  const int32_t* seq_tile;    // tile of sequence b (-1: it has no shared rows)
-  const int32_t* seq_row;     // its row there
-  float* records;             // [B * H + CTAs * kSharedRows][kRecordFloats]
+  SharedHead* head;     // null: no shared part
+  SharedTile* tiles;
+  int32_t* order;       // sequences, grouped by prefix
+  SharedSeq* seqs;      // by sequence
+  float* records;       // [B * H + CTAs * kSharedRows][kRecordFloats]
 };
 
 struct BalancedArgs {

@@ -54,19 +54,15 @@ constexpr int kGroupThreads = 1024;
 struct GroupArgs {
   int B, H, P;
   int64_t cap;
-  int ctas;
+  int ctas;  // of the attention
   const int32_t* shared_len;
   const int32_t* share_of;
-  SharedHead* head;
-  SharedTile* tiles;
-  int32_t* order;
-  int32_t* seq_tile;
-  int32_t* seq_row;
+  SharedTables t;
   int32_t* status;
 };
 
 struct Counts {
-  long long seqs, tiles, units;
+  int seqs, tiles, units;
 };
 
 __device__ __forceinline__ Counts plus(const Counts& a, const Counts& b) {
@@ -130,8 +126,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a)
     rank = __shfl_sync(0xffffffffu, rank, leader) + __popc(same & ((1u << lane) - 1));
     more |= p >= 0 && rank >= kSharedRows;
     if (b < a.B) {
-      a.seq_tile[b] = p;
-      a.seq_row[b] = rank;
+      a.t.seqs[b].first_seq = p;  // until the end: prefix and rank
+      a.t.seqs[b].row = rank;
     }
   }
   if (__syncthreads_or(more)) {
@@ -139,7 +135,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a)
     __syncthreads();
     for (int base = 0; base < a.B; base += threads) {
       const int b = base + tid;
-      const int p = b < a.B ? a.seq_tile[b] : -1;
+      const int p = b < a.B ? a.t.seqs[b].first_seq : -1;
       const unsigned same = __match_any_sync(0xffffffffu, p);
       const int leader = __ffs(same) - 1;
       int rank = 0;
@@ -151,7 +147,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a)
         __syncthreads();
       }
       rank = __shfl_sync(0xffffffffu, rank, leader) + __popc(same & ((1u << lane) - 1));
-      if (b < a.B) a.seq_row[b] = rank;
+      if (b < a.B) a.t.seqs[b].row = rank;
     }
   }
   Counts sum{0, 0, 0};  // so far
@@ -169,38 +165,45 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a)
     }
     const int nt = (n + kSharedRows - 1) / kSharedRows;
     const int keys = (len + kRows - 1) / kRows;
-    const long long each = (long long)keys * a.H;
+    const int each = keys * a.H;
     Counts total;
     const Counts at = plus(sum, block_scan(Counts{n, nt, nt * each}, scan, total));
     if (p < a.P) {
-      first[p] = (int)at.seqs;
-      tile0[p] = nt > 0 ? (int)at.tiles : -1;
+      first[p] = at.seqs;
+      tile0[p] = nt > 0 ? at.tiles : -1;
       for (int i = 0; i < nt; ++i) {
-        SharedTile t;
+        SharedTile t = {};
         t.first_unit = at.units + i * each;
-        t.first_seq = (int)at.seqs + i * kSharedRows;
+        t.first_seq = at.seqs + i * kSharedRows;
         t.rows = min(kSharedRows, n - i * kSharedRows);
         t.prefix = p;
         t.len = len;
         t.key_tiles = keys;
-        t.pad = 0;
-        a.tiles[at.tiles + i] = t;
+        a.t.tiles[at.tiles + i] = t;
       }
     }
     sum = plus(sum, total);
   }
   if (tid == 0) {
-    a.head->units = sum.units;
-    a.head->per = max(1ll, (sum.units + a.ctas - 1) / a.ctas);
-    a.head->tiles = (int)sum.tiles;
+    a.t.head->units = sum.units;
+    a.t.head->per = max(1, (sum.units + a.ctas - 1) / a.ctas);
+    a.t.head->tiles = sum.tiles;
   }
   __syncthreads();
   for (int b = tid; b < a.B; b += threads) {  // the rows this thread wrote above
-    const int p = a.seq_tile[b], rank = a.seq_row[b];
-    const bool has = p >= 0 && tile0[p] >= 0;
-    if (has) a.order[first[p] + rank] = b;
-    a.seq_tile[b] = has ? tile0[p] + rank / kSharedRows : -1;
-    a.seq_row[b] = rank % kSharedRows;
+    const int p = a.t.seqs[b].first_seq, rank = a.t.seqs[b].row;
+    SharedSeq q = {};
+    q.row = -1;
+    if (p >= 0 && tile0[p] >= 0) {
+      a.t.order[first[p] + rank] = b;
+      const SharedTile t = a.t.tiles[tile0[p] + rank / kSharedRows];
+      q.row = rank % kSharedRows;
+      q.first_seq = t.first_seq;
+      q.rows = t.rows;
+      q.key_tiles = t.key_tiles;
+      q.first_unit = t.first_unit;
+    }
+    a.t.seqs[b] = q;
   }
 }
 
@@ -244,16 +247,16 @@ __device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uin
 
 // A CTA's run of units as segments: key tiles [k0, k1) of head h of one tile of sequences.
 struct Walk {
-  long long u, end;
+  int u, end;
   int ti, h, k0, k1;
   SharedTile t;
 
   __device__ __forceinline__ bool begin(const SharedTables& tab) {
-    const long long per = tab.head->per, units = tab.head->units;
-    u = (long long)blockIdx.x * per;
-    end = min(u + per, units);
-    if (u >= end) return false;
-    int lo = 0, hi = tab.head->tiles - 1;  // the last tile whose first unit is at or before u
+    const SharedHead head = *tab.head;
+    if ((int64_t)blockIdx.x * head.per >= head.units) return false;
+    u = (int)blockIdx.x * head.per;
+    end = head.units - u > head.per ? u + head.per : head.units;
+    int lo = 0, hi = head.tiles - 1;  // the last tile whose first unit is at or before u
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (tab.tiles[mid].first_unit <= u)
@@ -263,9 +266,9 @@ struct Walk {
     }
     ti = lo;
     t = tab.tiles[ti];
-    h = (int)((u - t.first_unit) / t.key_tiles);
-    k0 = (int)((u - t.first_unit) % t.key_tiles);
-    k1 = (int)min((long long)t.key_tiles, k0 + (end - u));
+    h = (u - t.first_unit) / t.key_tiles;
+    k0 = (u - t.first_unit) % t.key_tiles;
+    k1 = min(t.key_tiles, k0 + (end - u));
     return true;
   }
   __device__ __forceinline__ bool next(const SharedTables& tab, int H) {
@@ -276,7 +279,7 @@ struct Walk {
       t = tab.tiles[++ti];
     }
     k0 = 0;
-    k1 = (int)min((long long)t.key_tiles, end - u);
+    k1 = min(t.key_tiles, end - u);
     return true;
   }
   __device__ __forceinline__ bool two() const { return t.rows > kRows; }  // a group takes its own rows
@@ -716,8 +719,7 @@ SharedPlan plan_shared(int B, int H, int P) {
   p.head = take(sizeof(SharedHead));
   p.tiles = take((size_t)most_tiles(B, P) * sizeof(SharedTile));
   p.order = take((size_t)B * 4);
-  p.seq_tile = take((size_t)B * 4);
-  p.seq_row = take((size_t)B * 4);
+  p.seqs = take((size_t)B * sizeof(SharedSeq));
   p.records = take(((size_t)B * H + (size_t)device_sm_count() * kSharedRows) * kRecordFloats * 4);
   p.bytes = off;
   return p;
@@ -735,11 +737,11 @@ cudaError_t launch_shared(const SharedLaunch& L, void* scratch, SharedTables* ta
   g.ctas = ctas;
   g.shared_len = L.shared_len;
   g.share_of = L.share_of;
-  g.head = reinterpret_cast<SharedHead*>(base + p.head);
-  g.tiles = reinterpret_cast<SharedTile*>(base + p.tiles);
-  g.order = reinterpret_cast<int32_t*>(base + p.order);
-  g.seq_tile = reinterpret_cast<int32_t*>(base + p.seq_tile);
-  g.seq_row = reinterpret_cast<int32_t*>(base + p.seq_row);
+  g.t.head = reinterpret_cast<SharedHead*>(base + p.head);
+  g.t.tiles = reinterpret_cast<SharedTile*>(base + p.tiles);
+  g.t.order = reinterpret_cast<int32_t*>(base + p.order);
+  g.t.seqs = reinterpret_cast<SharedSeq*>(base + p.seqs);
+  g.t.records = reinterpret_cast<float*>(base + p.records);
   g.status = L.status;
   static unsigned long long done[2] = {};
   cudaError_t e;
@@ -751,12 +753,7 @@ cudaError_t launch_shared(const SharedLaunch& L, void* scratch, SharedTables* ta
   fill_launch_config(cfg, attr, dim3(1), dim3(want < kGroupThreads ? want : kGroupThreads), tab, stream);
   if ((e = cudaLaunchKernelEx(&cfg, group_kernel, g)) != cudaSuccess) return e;
 
-  tables->head = g.head;
-  tables->tiles = g.tiles;
-  tables->order = g.order;
-  tables->seq_tile = g.seq_tile;
-  tables->seq_row = g.seq_row;
-  tables->records = reinterpret_cast<float*>(base + p.records);
+  *tables = g.t;
   AttnArgs a;
   a.B = L.B;
   a.H = L.H;

@@ -13,7 +13,7 @@ constexpr int kMaxShared = 8192;  // prefixes of a call (the grouping's shared-m
 
 // Offsets of the tables and records in launch_shared's scratch.
 struct SharedPlan {
-  size_t head, tiles, order, seq_tile, seq_row, records, bytes;
+  size_t head, tiles, order, seqs, records, bytes;
 };
 SharedPlan plan_shared(int B, int H, int P);
 

@@ -62,6 +62,7 @@ COMMON = [(dict(dims=None), INVALID, "dims"), (dict(dims=Dims(0, 4, 128, 128, 64
     (dict(score=Score(0.0, 0x10000, None, None)), INVALID, "slope and pos"),
     (dict(score=Score(0.0, None, 0x10000, None)), INVALID, "slope and pos"),
     (dict(score=Score(0.0, None, None, 0x10004)), INVALID, "range"),
+    (dict(dims=Dims(65535, 128, 128, 128, 2 ** 14)), UNSUPPORTED, "2^31 tiles"),
 ])
 def test_decode_scored_refusals(kw, code, word):
     got, msg = _scored(**kw)
@@ -72,7 +73,8 @@ def test_decode_scored_refusals(kw, code, word):
     (dict(sk=None), INVALID, "sk"), (dict(sv=MIS), INVALID, "aligned"), (dict(shared_len=None), INVALID, "shared_len"),
     (dict(share_of=None), INVALID, "share_of"), (dict(P=0), INVALID, "n_shared"), (dict(P=8193), INVALID, "n_shared"),
     (dict(cap=0), INVALID, "shared_cap"), (dict(cap=2 ** 30 + 1), INVALID, "shared_cap"),
-    (dict(P=8192, cap=2 ** 20), UNSUPPORTED, "2^31"),
+    (dict(P=8192, cap=2 ** 20), UNSUPPORTED, "2^31 shared rows"),
+    (dict(dims=Dims(65535, 128, 128, 128, 0), P=1, cap=2 ** 24 - 1), UNSUPPORTED, "units"),
 ])
 def test_decode_shared_refusals(kw, code, word):
     got, msg = _shared(**kw)

@@ -238,8 +238,15 @@ struct AttnArgs {
 };
 
 __device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (*reinterpret_cast<volatile int*>(&sm.abort_flag)) return false;
-  if (mbar_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&sm.abort_flag)) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+  }
   sm.abort_flag = 1;
   set_status(status, RSWA_DEVICE_WAIT_TIMEOUT);
   return false;
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.s_full[x], 1);
-      mbar_init(&sm.p_full[x], 128);
+      mbar_init(&sm.p_full[x], 4);  // one arrival a warp
       mbar_init(&sm.o_done[x], 1);
     }
     mbar_init(&sm.drain, 1);
@@ -620,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&sm.p_full[x]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[x]);
       }
       // ---- the segment's records ----
       const bool any = x < events;

@@ -190,10 +190,10 @@ def _want(t: torch.Tensor, name: str, dtype, shape=None):
     return t
 
 
-def _tensor(t, name: str, dtype, shape, device):
-    """A contiguous tensor of this dtype and shape on `device`: its address."""
+def _tensor(t, name: str, dtype, shape, index: int):
+    """A contiguous tensor of this dtype and shape on CUDA device `index`: its address."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -201,19 +201,20 @@ def _tensor(t, name: str, dtype, shape, device):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name}: must be contiguous")
 
 
-def _device_of(t, name: str):
+def _device_of(t, name: str) -> int:
+    """The CUDA device index of a tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
 # The raw handle of a device's current stream, without building a torch.cuda.Stream (2 us a call).
@@ -222,12 +223,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _fns: dict = {}
 
 
-def _call(name: str, device, stream, *args):
+def _call(name: str, index: int, stream, *args):
     """The C call on `stream` (default: the current stream of the tensors' device), with that device current."""
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(load(), name)
-    index = device.index
     if stream is None:
         raw = _raw_stream(index)
     else:
@@ -235,7 +235,7 @@ def _call(name: str, device, stream, *args):
     if torch.cuda.current_device() == index:
         code = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             code = fn(*args, raw)
     if code != 0:
         _check(name, code)
@@ -321,14 +321,14 @@ def rswa_rope_page2d(q, tok_pos, page, q_out=None, k=None, k_out=None, base: flo
     return q_out, k_out
 
 
-def _rope_rows(t, name: str, dtype, shape, device):
+def _rope_rows(t, name: str, dtype, shape, index: int):
     """The address of rows [B][H][T][D] or [B][H][D] in any order of their axes, the last one dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
@@ -962,13 +962,13 @@ def srswa_step_rope(q, k_new, v_new, q_idx, kbar, pk, pv, prefix_len, ring_k, ri
         _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
-def _workspace(t, device):
+def _workspace(t, index: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError("workspace: expected a torch.Tensor")
     if t.dtype is not torch.uint8:
         raise TypeError(f"workspace: expected torch.uint8, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"workspace: expected a tensor on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"workspace: expected a tensor on cuda:{index}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     return t.data_ptr(), t.numel()

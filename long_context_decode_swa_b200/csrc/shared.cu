@@ -8,7 +8,10 @@
 // key tile of 128 rows, some 2,700 cycles of one SM's share of HBM, against 512 cycles of MMA
 // and about 1,000 of exponentials); above that the exponentials.
 //
-// group_kernel (one CTA): sorts the sequences by prefix and lays the tables out. shared_kernel: one CTA an SM;
+// Grouping sorts the sequences by prefix and lays the tables out: a launch of one CTA (group_kernel), or,
+// with at most 384 sequences and prefixes, by every CTA of the attention for itself, which saves the
+// launch (3 us of a call's host time; eight sequences over one page 10.7 -> 10.0 us on the GPU).
+// shared_kernel: one CTA an SM;
 // the work is a line of units (a key tile of one head of one tile of sequences) cut evenly over the
 // CTAs, so few long prefixes fill the chip as well as many short ones. A CTA walks its run in
 // segments, one per (tile, head), with roles as in the chunked prefill:
@@ -211,6 +214,9 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const GroupArgs a)
 // attention
 // ---------------------------------------------------------------------------------------------
 
+constexpr int kSmallGroup = kThreads;  // sequences and prefixes that a CTA's threads take one each
+static_assert(5 * kSmallGroup * 4 + (kSmallGroup / 32) * 12 <= 8192, "group_small's scratch");
+
 struct SharedSmem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kKStages][kTileBytes];
@@ -235,7 +241,91 @@ struct AttnArgs {
   float scale_log2;
   SharedTables t;
   int32_t* status;
+  int group;     // 1: the tables are laid out in this launch, by group_small
+  GroupArgs g;
 };
+
+// group_kernel's tables for at most kSmallGroup sequences and prefixes, by the whole CTA. Every CTA
+// writes the same values and reads its own. scratch: 8 KiB of shared memory.
+__device__ void group_small(const GroupArgs& a, int* scratch) {
+  int* share = scratch;
+  int* first = scratch + kSmallGroup;      // of a prefix: its first place in order[],
+  int* tile0 = first + kSmallGroup;        // its first tile (-1: no rows, or nobody reads it),
+  int* unit0 = tile0 + kSmallGroup;        // its first unit
+  int* keys_of = unit0 + kSmallGroup;      // and its key tiles
+  Counts* sums = reinterpret_cast<Counts*>(keys_of + kSmallGroup);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int p = tid < a.B ? a.share_of[tid] : -1;
+  int len = tid < a.P ? a.shared_len[tid] : 0;
+  if (p < -1 || p >= a.P) {
+    if (blockIdx.x == 0) set_status(a.status, RSWA_DEVICE_BAD_SHARE);
+    p = -1;
+  }
+  share[tid] = p;
+  __syncthreads();
+  int rank = 0, n = 0;  // of sequence tid among its prefix's; sequences of prefix tid
+  for (int j = 0; j < a.B; j += 4) {
+    const int4 s4 = *reinterpret_cast<const int4*>(share + j);  // past B: -1
+    const int s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      rank += s[u] == p && j + u < tid;
+      n += s[u] == tid;
+    }
+  }
+  if (n > 0 && (len < 0 || len > a.cap)) {
+    if (blockIdx.x == 0) set_status(a.status, RSWA_DEVICE_BAD_PREFIX_LEN);
+    len = 0;
+  }
+  if (len <= 0) n = 0;
+  const int nt = (n + kSharedRows - 1) / kSharedRows;
+  const int keys = n > 0 ? (len + kRows - 1) / kRows : 0;
+  const Counts mine{n, nt, nt * keys * a.H};
+  const Counts inc = warp_scan(mine, lane);
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  Counts at{inc.seqs - mine.seqs, inc.tiles - mine.tiles, inc.units - mine.units}, total{0, 0, 0};
+  for (int w = 0; w < kSmallGroup / 32; ++w) {
+    if (w < warp) at = plus(at, sums[w]);
+    total = plus(total, sums[w]);
+  }
+  first[tid] = at.seqs;
+  tile0[tid] = nt > 0 ? at.tiles : -1;
+  unit0[tid] = at.units;
+  keys_of[tid] = keys;
+  for (int i = 0; i < nt; ++i) {
+    SharedTile t = {};
+    t.first_unit = at.units + i * keys * a.H;
+    t.first_seq = at.seqs + i * kSharedRows;
+    t.rows = min(kSharedRows, n - i * kSharedRows);
+    t.prefix = tid;
+    t.len = len;
+    t.key_tiles = keys;
+    a.t.tiles[at.tiles + i] = t;
+  }
+  if (tid == 0) {
+    a.t.head->units = total.units;
+    a.t.head->per = max(1, (total.units + a.ctas - 1) / a.ctas);
+    a.t.head->tiles = total.tiles;
+  }
+  __syncthreads();
+  if (tid < a.B) {
+    SharedSeq q = {};
+    q.row = -1;
+    if (p >= 0 && tile0[p] >= 0) {
+      const int i = rank / kSharedRows;
+      a.t.order[first[p] + rank] = tid;
+      q.row = rank % kSharedRows;
+      q.first_seq = first[p] + i * kSharedRows;
+      q.key_tiles = keys_of[p];
+      q.first_unit = unit0[p] + i * keys_of[p] * a.H;
+      q.rows = a.t.tiles[tile0[p] + i].rows;  // written by this CTA, before the barrier
+    }
+    a.t.seqs[tid] = q;
+  }
+  fence_async_smem();  // the scratch is a TMA destination next
+  __syncthreads();
+}
 
 __device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -353,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  griddep_wait();  // the tables come from the grouping launch
+  griddep_wait();  // the tables come from the grouping launch, or are laid out here
+  if (a.group) group_small(a.g, reinterpret_cast<int*>(sm.k[0]));
   griddep_launch_dependents();
 
   Walk w;
@@ -753,13 +844,16 @@ cudaError_t launch_shared(const SharedLaunch& L, void* scratch, SharedTables* ta
   g.status = L.status;
   static unsigned long long done[2] = {};
   cudaError_t e;
-  const size_t tab = (size_t)L.P * 12;
-  if ((e = ensure_smem_limit(group_kernel, (size_t)kMaxShared * 12, &done[0])) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  const int want = ((L.B > L.P ? L.B : L.P) + 31) / 32 * 32;
-  fill_launch_config(cfg, attr, dim3(1), dim3(want < kGroupThreads ? want : kGroupThreads), tab, stream);
-  if ((e = cudaLaunchKernelEx(&cfg, group_kernel, g)) != cudaSuccess) return e;
+  const bool small = L.B <= kSmallGroup && L.P <= kSmallGroup;
+  if (!small) {
+    const size_t tab = (size_t)L.P * 12;
+    if ((e = ensure_smem_limit(group_kernel, (size_t)kMaxShared * 12, &done[0])) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    const int want = ((L.B > L.P ? L.B : L.P) + 31) / 32 * 32;
+    fill_launch_config(cfg, attr, dim3(1), dim3(want < kGroupThreads ? want : kGroupThreads), tab, stream);
+    if ((e = cudaLaunchKernelEx(&cfg, group_kernel, g)) != cudaSuccess) return e;
+  }
 
   *tables = g.t;
   AttnArgs a;
@@ -770,6 +864,8 @@ cudaError_t launch_shared(const SharedLaunch& L, void* scratch, SharedTables* ta
   a.scale_log2 = L.scale * 1.4426950408889634f;
   a.t = *tables;
   a.status = L.status;
+  a.group = small;
+  a.g = g;
   CUtensorMap tk, tv;
   const int64_t rows = (int64_t)L.P * L.H * L.cap;
   if ((e = make_rows_map(&tk, L.sk, rows)) != cudaSuccess) return e;

@@ -78,6 +78,9 @@ class Case:
     (256, 1, 1, 300),
     (257, 1, 1, 300),      # a second pass over the prefix
     (600, 1, 2, 520),      # three
+    (384, 1, 1, 200),      # as many sequences as the attention groups by itself
+    (385, 2, 1, 200),      # one more
+    (384, 384, 1, 3), (5, 384, 1, 40), (5, 385, 1, 40),
     (64, 16, 16, 900),     # several segments a CTA
     (40, 3, 5, 5000),      # a prefix cut over many CTAs
 ])

@@ -98,10 +98,10 @@ def load(path: str | None = None):
         if path is None and p == _DEFAULT_LIB:
             from . import build as _build
             try:
-                if not _build.up_to_date():
+                if not (_build.up_to_date() and _build.ext_up_to_date()):
                     _build.build()
             except RuntimeError:
-                if not os.path.exists(p):
+                if not os.path.exists(p) or not os.path.exists(_build.EXT):
                     raise
         if not os.path.exists(p):
             raise RuntimeError(f"librswa.so not found at {p}; run python -m long_context_decode_swa_b200.build")
@@ -190,22 +190,25 @@ def _want(t: torch.Tensor, name: str, dtype, shape=None):
     return t
 
 
-def _tensor(t, name: str, dtype, shape, index: int):
-    """A contiguous tensor of this dtype and shape on CUDA device `index`: its address."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name}: must be contiguous")
+_native = None
+
+
+def _tensors():
+    """The native tensor checks (csrc/tensors.cpp): addresses(index, spec, ..) gives the data pointers of the
+    specs' tensors, each (tensor, name, dtype, shape): contiguous, of that dtype and shape, on CUDA device
+    `index`; a fifth element lets a tensor be None. strided() gives (pointer, strides) of any layout."""
+    global _native
+    if _native is None:
+        load()  # builds what is missing
+        from . import _tensors as native
+        _native = native
+    return _native
+
+
+@functools.lru_cache(maxsize=1024)
+def _dims(batch: int, heads: int, head_dim: int, ring: int, prefix_cap: int) -> Dims:
+    """A shared Dims of these values (read-only)."""
+    return Dims(batch, heads, head_dim, ring, prefix_cap)
 
 
 def _device_of(t, name: str) -> int:
@@ -321,19 +324,6 @@ def rswa_rope_page2d(q, tok_pos, page, q_out=None, k=None, k_out=None, base: flo
     return q_out, k_out
 
 
-def _rope_rows(t, name: str, dtype, shape, index: int):
-    """The address of rows [B][H][T][D] or [B][H][D] in any order of their axes, the last one dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
@@ -361,7 +351,7 @@ def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str =
     through. layout: "half" or "interleaved" pairs. inverse=True applies the transpose, which turns
     gradients back. Outputs default to in place. Returns (q_out, k_out)."""
     dev = _device_of(q, "q")
-    shape, dtype = q.shape, q.dtype
+    shape, dtype = tuple(q.shape), q.dtype
     if len(shape) not in (3, 4):
         raise ValueError("q: expected [B, H, T, D] or [B, H, D]")
     if dtype not in _ROPE_DTYPES:
@@ -371,14 +361,12 @@ def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str =
         raise TypeError("inv_freq: expected a contiguous 1-D float64 tensor on the CPU")
     if q_out is None:
         q_out = q
-    qp, qs = q.data_ptr(), q.stride()
-    qop, qos = _rope_rows(q_out, "q_out", dtype, shape, dev), q_out.stride()
-    if qp == qop and qs != qos:
-        raise ValueError("q_out: in place needs the input's strides")
-    pos_shape = shape[:1] if len(shape) == 3 else (shape[0], shape[2])
+    native = _tensors()
+    pos_p, = native.addresses(dev, (pos, "pos", torch.int32, shape[:1] if len(shape) == 3 else (shape[0], shape[2])))
     if k is None:
         if k_out is not None:
             raise ValueError("k_out given without k")
+        (qp, qs), (qop, qos) = native.strided(dev, (q, "q", dtype, shape), (q_out, "q_out", dtype, shape))
         d = _rope_desc(dtype, layout, mscale, inverse, inv_freq.shape[0], shape, 0, qs, qos)
         kp = kop = None
     else:
@@ -386,14 +374,16 @@ def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str =
             raise ValueError("k: expected a tensor shaped like q but for its heads (one at least)")
         if k_out is None:
             k_out = k
-        kshape = (shape[0], k.shape[1]) + tuple(shape[2:])
-        kp, ks = _rope_rows(k, "k", dtype, kshape, dev), k.stride()
-        kop, kos = _rope_rows(k_out, "k_out", dtype, kshape, dev), k_out.stride()
+        kshape = (shape[0], k.shape[1]) + shape[2:]
+        (qp, qs), (qop, qos), (kp, ks), (kop, kos) = native.strided(
+            dev, (q, "q", dtype, shape), (q_out, "q_out", dtype, shape), (k, "k", dtype, kshape),
+            (k_out, "k_out", dtype, kshape))
         if kp == kop and ks != kos:
             raise ValueError("k_out: in place needs the input's strides")
         d = _rope_desc(dtype, layout, mscale, inverse, inv_freq.shape[0], shape, kshape[1], qs, qos, ks, kos)
-    _call("rswa_rope_1d", dev, stream, d, inv_freq.data_ptr(), _tensor(pos, "pos", torch.int32, pos_shape, dev), qp,
-          qop, kp, kop)
+    if qp == qop and qs != qos:
+        raise ValueError("q_out: in place needs the input's strides")
+    _call("rswa_rope_1d", dev, stream, d, inv_freq.data_ptr(), pos_p, qp, qop, kp, kop)
     return q_out, k_out
 
 
@@ -962,38 +952,16 @@ def srswa_step_rope(q, k_new, v_new, q_idx, kbar, pk, pv, prefix_len, ring_k, ri
         _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
-def _workspace(t, index: int):
+def _numel(t, name: str) -> int:
     if not isinstance(t, torch.Tensor):
-        raise TypeError("workspace: expected a torch.Tensor")
-    if t.dtype is not torch.uint8:
-        raise TypeError(f"workspace: expected torch.uint8, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"workspace: expected a tensor on cuda:{index}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
-    return t.data_ptr(), t.numel()
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    return t.numel()
 
 
-def _score(softcap, slopes, pos, ranges, heads: int, lead, device):
-    """rswa_score of queries [*lead]: slopes [heads] with pos [B], ranges [*lead, 2]."""
-    if slopes is not None and pos is None:
-        raise ValueError("slopes need pos")
-    s = Score(softcap, None, None, None)
-    if slopes is not None:
-        s.slope = _tensor(slopes, "slopes", torch.float32, (heads,), device)
-        s.pos = _tensor(pos, "pos", torch.int32, lead[:1], device)
-    if ranges is not None:
-        s.range = _tensor(ranges, "ranges", torch.int32, (*lead, 2), device)
-    return s
-
-
-def _ring(ring_k, ring_v, wp, fill, B: int, H: int, D: int, device):
+def _ring_shape(ring_k, B: int, H: int, D: int):
     if not isinstance(ring_k, torch.Tensor) or ring_k.dim() != 4:
         raise ValueError("ring_k: expected a tensor [B, H, n, D]")
-    shape = (B, H, ring_k.shape[2], D)
-    return (_tensor(ring_k, "ring_k", torch.bfloat16, shape, device),
-            _tensor(ring_v, "ring_v", torch.bfloat16, shape, device),
-            _tensor(wp, "wp", torch.int32, (B,), device), _tensor(fill, "fill", torch.int32, (B,), device))
+    return (B, H, ring_k.shape[2], D)
 
 
 def rswa_decode_scored(q, pk, pv, prefix_len, ring_k, ring_v, wp, fill, out, workspace, softcap: float = 0.0,
@@ -1005,17 +973,22 @@ def rswa_decode_scored(q, pk, pv, prefix_len, ring_k, ring_v, wp, fill, out, wor
     dev = _device_of(q, "q")
     if q.dim() != 3 or not isinstance(pk, torch.Tensor) or pk.dim() != 4:
         raise ValueError("expected q [B, H, D] and pk [B, H, cap, D]")
-    B, H, D = q.shape
-    cap = pk.shape[2]
+    if slopes is None:
+        pos = None
+    elif pos is None:
+        raise ValueError("slopes need pos")
+    B, H, D = row = tuple(q.shape)
+    prefix = (B, H, pk.shape[2], D)
+    ring = _ring_shape(ring_k, B, H, D)
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    rk, rv, w, f = _ring(ring_k, ring_v, wp, fill, B, H, D, dev)
-    score = _score(softcap, slopes, pos, ranges, H, (B,), dev)
-    wsp, wsn = _workspace(workspace, dev)
-    _call("rswa_decode_scored", dev, stream, Dims(B, H, D, ring_k.shape[2], cap), score, _tensor(q, "q", bf16, (B, H, D), dev),
-          _tensor(pk, "pk", bf16, (B, H, cap, D), dev), _tensor(pv, "pv", bf16, (B, H, cap, D), dev),
-          _tensor(prefix_len, "prefix_len", i32, (B,), dev), rk, rv, w, f,
-          1.0 / math.sqrt(D) if scale is None else scale, _tensor(out, "out", f32, (B, H, D), dev),
-          None if lse is None else _tensor(lse, "lse", f32, (B, H), dev), wsp, wsn)
+    ws_bytes = _numel(workspace, "workspace")
+    a = _tensors().addresses(dev, (q, "q", bf16, row), (pk, "pk", bf16, prefix), (pv, "pv", bf16, prefix),
+                   (prefix_len, "prefix_len", i32, (B,)), (ring_k, "ring_k", bf16, ring), (ring_v, "ring_v", bf16, ring),
+                   (wp, "wp", i32, (B,)), (fill, "fill", i32, (B,)), (out, "out", f32, row), (lse, "lse", f32, (B, H), True),
+                   (workspace, "workspace", torch.uint8, (ws_bytes,)), (slopes, "slopes", f32, (H,), True),
+                   (pos, "pos", i32, (B,), True), (ranges, "ranges", i32, (B, 2), True))
+    _call("rswa_decode_scored", dev, stream, _dims(B, H, D, ring[2], prefix[2]), Score(softcap, *a[11:]), *a[:8],
+          1.0 / math.sqrt(D) if scale is None else scale, *a[8:11], ws_bytes)
 
 
 def rswa_prefill_scored(q, k_out, v_out, pk, pv, prefix_len, out, workspace, softcap: float = 0.0, slopes=None,
@@ -1028,25 +1001,32 @@ def rswa_prefill_scored(q, k_out, v_out, pk, pv, prefix_len, out, workspace, sof
     dev = _device_of(q, "q")
     if q.dim() != 4 or not isinstance(pk, torch.Tensor) or pk.dim() != 4:
         raise ValueError("expected q [B, H, T, D] and pk [B, H, cap, D]")
-    B, H, T, D = q.shape
-    cap = pk.shape[2]
-    bf16, i32 = torch.bfloat16, torch.int32
-    rk = rv = w = f = None
+    if slopes is None:
+        pos = None
+    elif pos is None:
+        raise ValueError("slopes need pos")
+    B, H, T, D = rows = tuple(q.shape)
+    prefix = (B, H, pk.shape[2], D)
     if ring_k is not None:
-        rk, rv, w, f = _ring(ring_k, ring_v, wp, fill, B, H, D, dev)
-        n = ring_k.shape[2]
+        ring_shape = _ring_shape(ring_k, B, H, D)
+        n = ring_shape[2]
     else:
         if ring is None:
             raise ValueError("without a ring tensor, pass the window length as ring=n")
-        n = int(ring)
-    score = _score(softcap, slopes, pos, ranges, H, (B, T), dev)
-    wsp, wsn = _workspace(workspace, dev)
-    _call("rswa_prefill_scored", dev, stream, Dims(B, H, D, n, cap), score, T, _tensor(q, "q", bf16, (B, H, T, D), dev),
-          _tensor(k_out, "k_out", bf16, (B, H, T, D), dev), _tensor(v_out, "v_out", bf16, (B, H, T, D), dev),
-          _tensor(pk, "pk", bf16, (B, H, cap, D), dev), _tensor(pv, "pv", bf16, (B, H, cap, D), dev),
-          _tensor(prefix_len, "prefix_len", i32, (B,), dev), rk, rv, w, f, 1.0 / math.sqrt(D) if scale is None else scale,
-          _tensor(out, "out", bf16, (B, H, T, D), dev),
-          None if lse is None else _tensor(lse, "lse", torch.float32, (B, H, T), dev), 1 if write_ring else 0, wsp, wsn)
+        if ring_v is not None or wp is not None or fill is not None:
+            raise ValueError("ring_k, ring_v, wp and fill go together")
+        n, ring_shape = int(ring), ()
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    ws_bytes = _numel(workspace, "workspace")
+    ring_specs = ((ring_k, "ring_k", bf16, ring_shape), (ring_v, "ring_v", bf16, ring_shape), (wp, "wp", i32, (B,)),
+                  (fill, "fill", i32, (B,))) if ring_k is not None else ((None, "", i32, (), True),) * 4
+    a = _tensors().addresses(dev, (q, "q", bf16, rows), (k_out, "k_out", bf16, rows), (v_out, "v_out", bf16, rows),
+                   (pk, "pk", bf16, prefix), (pv, "pv", bf16, prefix), (prefix_len, "prefix_len", i32, (B,)), *ring_specs,
+                   (out, "out", bf16, rows), (lse, "lse", f32, (B, H, T), True),
+                   (workspace, "workspace", torch.uint8, (ws_bytes,)), (slopes, "slopes", f32, (H,), True),
+                   (pos, "pos", i32, (B,), True), (ranges, "ranges", i32, (B, T, 2), True))
+    _call("rswa_prefill_scored", dev, stream, _dims(B, H, D, n, prefix[2]), Score(softcap, *a[13:]), T, *a[:10],
+          1.0 / math.sqrt(D) if scale is None else scale, *a[10:12], 1 if write_ring else 0, a[12], ws_bytes)
 
 
 def shared_workspace_bytes(dims: Dims, n_shared: int) -> int:
@@ -1071,24 +1051,25 @@ def rswa_decode_shared(q, sk, sv, shared_len, share_of, ring_k, ring_v, wp, fill
     dev = _device_of(q, "q")
     if q.dim() != 3 or not isinstance(sk, torch.Tensor) or sk.dim() != 4:
         raise ValueError("expected q [B, H, D] and sk [P, H, cap, D]")
-    B, H, D = q.shape
-    P, _, scap, _ = sk.shape
+    B, H, D = row = tuple(q.shape)
+    P, scap = sk.shape[0], sk.shape[2]
+    shared = (P, H, scap, D)
+    ring = _ring_shape(ring_k, B, H, D)
     bf16, i32 = torch.bfloat16, torch.int32
-    cap, kp, vp, np_ = 0, None, None, None
     if pk is not None:
         if not isinstance(pk, torch.Tensor) or pk.dim() != 4:
             raise ValueError("pk: expected a tensor [B, H, cap, D]")
-        cap = pk.shape[2]
-        kp = _tensor(pk, "pk", bf16, (B, H, cap, D), dev)
-        vp = _tensor(pv, "pv", bf16, (B, H, cap, D), dev)
-        np_ = _tensor(prefix_len, "prefix_len", i32, (B,), dev)
-    elif pv is not None or prefix_len is not None:
-        raise ValueError("pk, pv and prefix_len go together")
-    rk, rv, w, f = _ring(ring_k, ring_v, wp, fill, B, H, D, dev)
-    wsp, wsn = _workspace(workspace, dev)
-    _call("rswa_decode_shared", dev, stream, Dims(B, H, D, ring_k.shape[2], cap), P, scap,
-          _tensor(q, "q", bf16, (B, H, D), dev), _tensor(sk, "sk", bf16, (P, H, scap, D), dev),
-          _tensor(sv, "sv", bf16, (P, H, scap, D), dev), _tensor(shared_len, "shared_len", i32, (P,), dev),
-          _tensor(share_of, "share_of", i32, (B,), dev), kp, vp, np_, rk, rv, w, f,
-          1.0 / math.sqrt(D) if scale is None else scale, _tensor(out, "out", bf16, (B, H, D), dev),
-          None if lse is None else _tensor(lse, "lse", torch.float32, (B, H), dev), wsp, wsn)
+        prefix = (B, H, pk.shape[2], D)
+        private = ((pk, "pk", bf16, prefix), (pv, "pv", bf16, prefix), (prefix_len, "prefix_len", i32, (B,)))
+    else:
+        if pv is not None or prefix_len is not None:
+            raise ValueError("pk, pv and prefix_len go together")
+        prefix, private = (B, H, 0, D), ((None, "", i32, (), True),) * 3
+    ws_bytes = _numel(workspace, "workspace")
+    a = _tensors().addresses(dev, (q, "q", bf16, row), (sk, "sk", bf16, shared), (sv, "sv", bf16, shared),
+                   (shared_len, "shared_len", i32, (P,)), (share_of, "share_of", i32, (B,)), *private,
+                   (ring_k, "ring_k", bf16, ring), (ring_v, "ring_v", bf16, ring), (wp, "wp", i32, (B,)),
+                   (fill, "fill", i32, (B,)), (out, "out", bf16, row), (lse, "lse", torch.float32, (B, H), True),
+                   (workspace, "workspace", torch.uint8, (ws_bytes,)))
+    _call("rswa_decode_shared", dev, stream, _dims(B, H, D, ring[2], prefix[2]), P, scap, *a[:12],
+          1.0 / math.sqrt(D) if scale is None else scale, *a[12:], ws_bytes)

@@ -1,4 +1,5 @@
-"""Builds librswa.so in-tree from csrc/*.cu for sm_100a with nvcc.
+"""Builds librswa.so in-tree from csrc/*.cu for sm_100a with nvcc, and the binding's tensor
+checks (_tensors.so, from csrc/tensors.cpp) with g++.
 
 Run as ``python -m long_context_decode_swa_b200.build`` or call ``build()``.
 Objects go to ``long_context_decode_swa_b200/_build/`` and the library to
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librswa.so")
+EXT_SRC = os.path.join(CSRC, "tensors.cpp")
+EXT = os.path.join(PKG, "_tensors.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -49,7 +52,34 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def ext_up_to_date() -> bool:
+    return os.path.exists(EXT) and os.path.getmtime(EXT_SRC) <= os.path.getmtime(EXT)
+
+
+def build_ext(force: bool = False) -> str:
+    """The CPython extension that checks tensors (no CUDA in it)."""
+    if not force and ext_up_to_date():
+        return EXT
+    import sysconfig
+
+    import torch
+    # torch's own header and library folders, without importing its extension builder (which looks for a GPU)
+    home = os.path.dirname(torch.__file__)
+    includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"]]
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-I{d}" for d in includes], EXT_SRC, "-o", tmp, f"-L{os.path.join(home, 'lib')}", "-ltorch_python",
+           "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
+    build_ext(force)
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

@@ -128,7 +128,7 @@ RSWA_API rswa_status rswa_check_status(void* workspace, size_t ws_bytes, int32_t
  * in flight land (bounded by the same limit) and ends the CTA, so the call returns and
  * the CUDA context stays usable. This call arms, for the NEXT decode-family call made
  * by the calling host thread only (rswa_decode*, srswa_decode*, srswa_prefill,
- * rswa_decode_noalloc; consumed by that call even if it fails validation):
+ * rswa_decode_noalloc; of rswa_decode_shared, its private part; consumed by that call even if it fails validation):
  *   drop_tile     : >= 0: CTA 0 neither arms nor fills the shared-memory stage of its
  *                   CTA-local tile number drop_tile, so that tile's bounded wait runs
  *                   out (no copy is in flight for it); -1: nothing dropped.
@@ -601,7 +601,7 @@ RSWA_API rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_fre
  * (the newest slot is the query's own token, as after rswa_append).
  * Arguments as rswa_decode (workspace: RSWA_OP_DECODE_SCORED), and
  *   score : host pointer, read during the call only
- *     softcap : finite, >= 0
+ *     softcap : 0 (none) or in [1e-3, 1e6]
  *     slope   : f32 [heads] device array of finite values, or NULL (no distance bias)
  *     pos     : int32 [batch] device array, with slope: each in [0, 2^30] (others: flagged
  *               RSWA_DEVICE_BAD_POS, the sequence's prefix is skipped); NULL without

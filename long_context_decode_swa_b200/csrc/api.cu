@@ -1111,6 +1111,11 @@ static rswa_status balanced_args(const char* fn, const rswa_dims* dims, const vo
                                  const int32_t* prefix_len, const void* ring_k, const void* ring_v, const int32_t* wp,
                                  const int32_t* fill, float scale, void* out, float* lse, void* workspace,
                                  rswa::BalancedArgs* a) {
+  // a wait-timeout test knob applies to this call only, whether or not it launches
+  const int test_drop_tile = g_test_drop_tile;
+  const uint64_t test_wait_ns = g_test_wait_ns;
+  g_test_drop_tile = -1;
+  g_test_wait_ns = 0;
   rswa_status st = check_dims(fn, dims, true);
   if (st != RSWA_OK) return st;
   REQUIRE_PTR(q);
@@ -1145,14 +1150,17 @@ static rswa_status balanced_args(const char* fn, const rswa_dims* dims, const vo
   a->out = out;
   a->lse = lse;
   a->status = ws_status(workspace);
+  a->wait_limit_ns = test_wait_ns > 0 ? test_wait_ns : rswa::kWaitLimitNs;
+  a->drop_tile = test_drop_tile;
   return RSWA_OK;
 }
 
 // A score's own checks.
 static rswa_status check_score(const char* fn, const rswa_score* s) {
   if (s == nullptr) return fail(RSWA_ERR_INVALID, "%s: score must not be NULL", fn);
-  if (!(s->softcap >= 0.f) || !std::isfinite(s->softcap))
-    return fail(RSWA_ERR_INVALID, "%s: softcap must be finite and >= 0", fn);
+  // outside this range scale / softcap and softcap log2(e) leave the f32 range for some scale
+  if (!(s->softcap == 0.f || (s->softcap >= 1e-3f && s->softcap <= 1e6f)))
+    return fail(RSWA_ERR_INVALID, "%s: softcap must be 0 or in [1e-3, 1e6]", fn);
   if ((s->slope == nullptr) != (s->pos == nullptr))
     return fail(RSWA_ERR_INVALID, "%s: slope and pos must both be given or both be NULL", fn);
   if (s->range != nullptr && (reinterpret_cast<uintptr_t>(s->range) & 7u) != 0)

@@ -60,10 +60,12 @@ struct BalancedSmem {
   int is_last;
 };
 
+// (Inputs are read through L2: with a shared part this launch starts while the one before it runs, so
+// that no launch boundary has cleared what an L1 holds since the inputs were written.)
 template <bool kScored>
 __device__ __forceinline__ SeqRows rows_of(const BalancedArgs& a, int b, bool report) {
   SeqRows s;
-  int m = a.cap > 0 ? a.prefix_len[b] : 0;
+  int m = a.cap > 0 ? __ldcg(a.prefix_len + b) : 0;
   if (m < 0 || m > a.cap) {
     if (report) set_status(a.status, RSWA_DEVICE_BAD_PREFIX_LEN);
     m = 0;
@@ -71,7 +73,7 @@ __device__ __forceinline__ SeqRows rows_of(const BalancedArgs& a, int b, bool re
   s.lo = 0;
   s.hi = m;
   if (kScored && a.ranges != nullptr) {
-    const int2 r = a.ranges[b];
+    const int2 r = __ldcg(a.ranges + b);
     if (r.x >= r.y) {
       s.hi = 0;
     } else if (r.x < 0 || r.y > m) {
@@ -83,13 +85,13 @@ __device__ __forceinline__ SeqRows rows_of(const BalancedArgs& a, int b, bool re
     }
   }
   if (kScored && a.slopes != nullptr) {
-    const int p = a.pos[b];
+    const int p = __ldcg(a.pos + b);
     if (p < 0 || p > kMaxPos) {
       if (report) set_status(a.status, RSWA_DEVICE_BAD_POS);
       s.lo = s.hi = 0;
     }
   }
-  int w = a.wp[b], f = a.fill[b];
+  int w = __ldcg(a.wp + b), f = __ldcg(a.fill + b);
   if (w < 0 || w >= a.n || f < 0 || f > a.n) {
     if (report) set_status(a.status, RSWA_DEVICE_BAD_RING_STATE);
     w = f = 0;
@@ -132,6 +134,7 @@ __device__ __forceinline__ void advance(const BalancedArgs& a, Cursor& c) {
 
 struct Tile {
   int rows;  // 0: empty, nothing was copied
+  bool armed;  // its copy was issued (all but the tile that a wait-timeout test drops)
   int row0;  // first prefix row (>= 0), or ~ of the first ring slot
 };
 
@@ -142,6 +145,7 @@ __device__ __forceinline__ Tile issue(const BalancedArgs& a, BalancedSmem& sm, i
   Tile t;
   t.rows = 0;
   t.row0 = 0;
+  t.armed = false;
   if (!share.whole && u >= share.units) return t;
   while (c.first < share.units && u >= c.first + c.s.tiles) advance<kScored>(a, c);
   if (c.first >= share.units) return t;
@@ -170,6 +174,9 @@ __device__ __forceinline__ Tile issue(const BalancedArgs& a, BalancedSmem& sm, i
     k = a.ring_k + off;
     v = a.ring_v + off;
   }
+  // a wait-timeout test: CTA 0 neither arms nor fills the stage of its unit drop_tile
+  if (a.drop_tile >= 0 && blockIdx.x == 0 && u == a.drop_tile) return t;
+  t.armed = t.rows > 0;
   if (t.rows > 0 && lane == 0) {
     const uint32_t bytes = (uint32_t)t.rows * kRowBytes;
     mbar_arrive_expect_tx(&sm.full[warp], 2 * bytes);
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
   Tile tile = issue<kScored>(a, sm, u, share, ahead, warp, lane);
   SharedSeq seq;
   int seq_b = -1, shared_per = 1;
-  uint4 q_next = *reinterpret_cast<const uint4*>(a.q + ((int64_t)at.b * a.H + at.h) * kHeadDim + c * 8);
+  uint4 q_next = __ldcg(reinterpret_cast<const uint4*>(a.q + ((int64_t)at.b * a.H + at.h) * kHeadDim + c * 8));
   uint32_t phase = 0;
   bool ok = true;
 
@@ -443,9 +450,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
       sc.wp = at.s.wp;
       sc.n = a.n;
       if (a.slopes != nullptr) {
-        const float slope = a.slopes[at.h];
+        const float slope = __ldcg(a.slopes + at.h);
         sc.slope_log2 = slope * kLog2e;
-        sc.pos = a.pos[at.b];
+        sc.pos = __ldcg(a.pos + at.b);
         // distances are taken from the favoured end of the rows seen, an integer, so that far
         // documents keep the bias small where it counts; the log-sum-exp adds it back
         const int ring = at.s.len0 + at.s.len1;
@@ -463,13 +470,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
       for (int e = 0; e < 4; ++e) q2[e] = make_float2(bf16lo(ws[e]) * qmul, bf16hi(ws[e]) * qmul);
     }
     if (bh + 1 < (int64_t)a.B * a.H)  // the next item's query, while this one streams
-      q_next = *reinterpret_cast<const uint4*>(a.q + (bh + 1) * kHeadDim + c * 8);
+      q_next = __ldcg(reinterpret_cast<const uint4*>(a.q + (bh + 1) * kHeadDim + c * 8));
     State st;
     clear(st);
     for (; ok && u < end; u += step) {
       const Tile cur = tile;
       if (cur.rows > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp], phase))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp], phase, a.wait_limit_ns))) {
           if (lane == 0) set_status(a.status, RSWA_DEVICE_WAIT_TIMEOUT);
           ok = false;
           break;
@@ -599,9 +606,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) balanced_kernel(const __
     if (__syncthreads_or(!ok) || !ends || end >= share.units) break;
     advance<kScored>(a, at);
   }
-  // after a give-up the copy issued last may be in flight: let it land (bounded) before the
-  // shared memory goes away
-  if (!ok && tile.rows > 0) mbar_wait(&sm.full[warp], phase);
+  // after a give-up, this warp's or another's of its CTA, the copy issued last may be in flight: let it
+  // land (bounded) before the shared memory goes away (after a normal end none is)
+  if (tile.armed) mbar_wait(&sm.full[warp], phase, a.wait_limit_ns);
 }
 
 }  // namespace

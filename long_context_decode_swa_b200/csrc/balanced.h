@@ -66,6 +66,9 @@ struct BalancedArgs {
   const int32_t* pos;      // [B], with slopes
   const int2* ranges;      // [B] or null: the whole prefix
   SharedTables shared;
+  // as in DecodeArgs: the limit of every wait, and a test's dropped unit of CTA 0 (-1: none)
+  uint64_t wait_limit_ns;
+  int drop_tile;
   // set by launch_balanced
   int32_t* counters;
   float* records;

@@ -150,7 +150,7 @@ __device__ __forceinline__ bool tile_visible(const Ctx& c, int X, int kind, int 
 __device__ __forceinline__ int2 range_of(const Args& a, int m, int b, int i, bool report) {
   if (i >= a.T) return make_int2(0, 0);
   if (a.ranges == nullptr) return make_int2(0, m);
-  const int2 r = a.ranges[(int64_t)b * a.T + i];
+  const int2 r = __ldcg(a.ranges + (int64_t)b * a.T + i);
   if (r.x >= r.y) return make_int2(0, 0);
   if (r.x < 0 || r.y > m) {
     if (report) set_status(a.status, RSWA_DEVICE_BAD_RANGE);
@@ -463,13 +463,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 0) {
     // ---- the CTA's key tiles ----
     const bool first = qt == 0 && rank == 0 && h == 0 && lane == 0;
-    int m = a.cap > 0 ? a.prefix_len[b] : 0;
+    // (inputs through L2: a late launch starts while its first part runs, past no launch boundary
+    // that would have cleared what an L1 holds since they were written)
+    int m = a.cap > 0 ? __ldcg(a.prefix_len + b) : 0;
     if (m < 0 || m > a.cap) {
       if (first) set_status(a.status, RSWA_DEVICE_BAD_PREFIX_LEN);
       m = 0;
     }
     if (kBias) {
-      const int p = a.pos[b];
+      const int p = __ldcg(a.pos + b);
       if (p < 0 || p > kMaxPos) {
         if (first) set_status(a.status, RSWA_DEVICE_BAD_POS);
         m = 0;
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       c.wp = c.fill = 0;
       if (runs == 0) c.tile0[0] = 0;
       if (a.has_ring) {
-        const int w = a.wp[b], f = a.fill[b];
+        const int w = __ldcg(a.wp + b), f = __ldcg(a.fill + b);
         if (w < 0 || w >= a.n || f < 0 || f > a.n) {
           if (first) set_status(a.status, RSWA_DEVICE_BAD_RING_STATE);
         } else {
@@ -782,9 +784,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     float slope2 = 0.f;
     int pos = 0, ref = 0;  // ref: the distance of the row's most favoured key, taken off all of them
     if (kBias) {
-      const float slope = a.slopes[h];
+      const float slope = __ldcg(a.slopes + h);
       slope2 = slope * kLog2e;
-      pos = a.pos[b] + i;
+      pos = __ldcg(a.pos + b) + i;
       const bool pre = range.y > range.x;
       if (slope >= 0.f)
         ref = pre ? min(0, pos - (range.y - 1)) : 0;

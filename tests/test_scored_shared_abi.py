@@ -59,6 +59,7 @@ COMMON = [(dict(dims=None), INVALID, "dims"), (dict(dims=Dims(0, 4, 128, 128, 64
     (dict(score=None), INVALID, "score"), (dict(score=Score(-1.0, None, None, None)), INVALID, "softcap"),
     (dict(score=Score(math.nan, None, None, None)), INVALID, "softcap"),
     (dict(score=Score(math.inf, None, None, None)), INVALID, "softcap"),
+    (dict(score=Score(1e-4, None, None, None)), INVALID, "softcap"), (dict(score=Score(1e7, None, None, None)), INVALID, "softcap"),
     (dict(score=Score(0.0, 0x10000, None, None)), INVALID, "slope and pos"),
     (dict(score=Score(0.0, None, 0x10000, None)), INVALID, "slope and pos"),
     (dict(score=Score(0.0, None, None, 0x10004)), INVALID, "range"),

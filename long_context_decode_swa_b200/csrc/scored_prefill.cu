@@ -20,7 +20,7 @@
 // packed documents so costs what its documents cost, not what the prefix does.
 //
 // Scores: the special-function unit (16 a cycle and SM) bounds the kernel: one ex2 a score is 1,024
-// cycles a tile against 512 of MMA. tanh(u) = 1 - 2 / (e^2u + 1) would cost two more; where a warp's
+// cycles a tile, as many as its MMAs take. tanh(u) = 1 - 2 / (e^2u + 1) would cost two more; where a warp's
 // scores all have |u| = |scale q.k| / cap <= 0.4 (or 1), tanh is u times a minimax polynomial in u^2
 // instead, on the packed FMA pipe (errors below 1e-7 of the cap either way).
 #include <cuda.h>
@@ -563,6 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       c.jt0 = jlo > 0 ? jlo / kRows : 0;
       const int all = np + c.nr + min(i0 + kCtaRows - 1, a.T - 1) / kRows - c.jt0 + 1;
       c.total = kSplit ? (all - rank + cluster - 1) / cluster : all;  // key tiles rank, rank + cluster, ...
+      // a CTA of this launch gave up on a wait: no work (the output is flagged invalid)
+      if (*reinterpret_cast<volatile int32_t*>(a.status) & RSWA_DEVICE_WAIT_TIMEOUT) c.total = 0;
     }
   }
   tc_fence_before();
@@ -793,6 +795,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         ref = max(min(i + c.fill, c.n - 1), pre ? pos - range.x : 0);
     }
+    // Where the bias changes by at most 2^32 along a thread's columns, the largest raw score and the largest
+    // bias bound the row's maximum closely enough: its weights stay above 2^-41, far from fp32's least.
+    // (Paired only: 382 -> 358 us at 16 heads x 2368 queries x 10272 rows; a split chunk of 3 x 333 queries
+    // over documents, where few tiles are seen whole, took 64 us with it and takes 57 without.)
+    const bool gentle = fabsf(slope2) * (float)(kHalf - 1) <= 32.f;
     // l sums the unrounded weights, for O and lse alike: where one key dominates, O is off by the
     // rounding of its weight (at most half a bf16 step, as the output's own rounding); summing the
     // rounded ones too cost three more instructions a score pair
@@ -824,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool fused = false;
       float tmax = -INFINITY;
       if (ok && !none) {
-        if (!kBias && full) {
+        if (full && (!kBias || (!kSplit && gentle && rt.cut >= kRows))) {
           float lowest = INFINITY, highest = -INFINITY;
 #pragma unroll 1
           for (int ch = 0; ch < 2; ++ch) {
@@ -834,9 +841,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kCap) lowest = lowest_of(v, lowest);
           }
           if (kCap) how = tanh_of(lowest, highest, mul);
-          // without a mask or a bias the raw maximum is the maximum, and the scoring joins the exponentials' loop
+          // without a mask the raw maximum gives the maximum (a bound of it, where a bias is added), and the
+          // scoring joins the exponentials' loop
           fused = !kCap || how != kExact;
           tmax = kCap ? cap2 * tanhf(highest * mul) : highest * mul;
+          if (kBias) tmax += fmaf(fmaxf(slope2, 0.f), (float)(kHalf - 1), -slope2 * (float)(rt.base - col0));
         }
         if (!fused) {
           tmax = -INFINITY;
@@ -890,15 +899,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const float2 minus_m = splat(m_used == -INFINITY ? 0.f : -m_used);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-        auto weights = [&](auto&& less_m) {  // less_m: a pair of s -> score - m
+        auto weights = [&](auto&& less_m) {  // less_m: a pair of s, what is added to it -> score - m
 #pragma unroll 1
           for (int ch = 0; ch < 2; ++ch) {
             float v[32];
             load(ch, v);
             uint32_t pk[16];
+            const float c0 = kBias && !kSplit ? fmaf(-slope2, (float)(rt.base - col0 - ch * 32), minus_m.x) : 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float2 z2 = less_m(make_float2(v[2 * e], v[2 * e + 1]));
+              const float2 add = kBias && !kSplit && fused ? make_float2(fmaf(slope2, (float)(2 * e), c0), fmaf(slope2, (float)(2 * e + 1), c0)) : minus_m;
+              const float2 z2 = less_m(make_float2(v[2 * e], v[2 * e + 1]), add);
               const float2 p2 = make_float2(ex2(z2.x), ex2(z2.y));
               const __nv_bfloat162 pb = __floats2bfloat162_rn(p2.x, p2.y);
               pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
@@ -910,14 +921,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(s_cols + (uint32_t)ch * 16u, pk);
           }
         };
-        if (!fused)
-          weights([&](float2 z) { return __fadd2_rn(z, minus_m); });
+        if (!fused)  // (a split biased chunk's only way)
+          weights([&](float2 z, float2) { return __fadd2_rn(z, minus_m); });
         else if (!kCap)
-          weights([&](float2 z) { return __ffma2_rn(z, splat(mul), minus_m); });
+          weights([&](float2 z, float2 add) { return __ffma2_rn(z, splat(mul), add); });
         else if (how == kSmall)
-          weights([&](float2 z) { return capped_pair<TanhSmall>(z, mul, cap2, minus_m); });
+          weights([&](float2 z, float2 add) { return capped_pair<TanhSmall>(z, mul, cap2, add); });
         else
-          weights([&](float2 z) { return capped_pair<TanhMid>(z, mul, cap2, minus_m); });
+          weights([&](float2 z, float2 add) { return capped_pair<TanhMid>(z, mul, cap2, add); });
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
       tmem_wait_st();

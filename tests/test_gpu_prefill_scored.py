@@ -177,6 +177,15 @@ def test_bias_across_a_far_document(cuda_lib, slope):
     c.check(*c.run(), rel=8e-3)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 50.0])
+def test_gentle_and_steep_slopes_of_many_queries(cuda_lib, softcap):
+    # more 256-query tiles than SMs; where a slope moves the bias little along a tile, the tile's largest
+    # score is bounded rather than found
+    slopes = [0.7, -0.7, 0.34, -0.34, 0.36, -0.36, 0.02, -0.02, 0.0, 4.0, -4.0] * 7
+    c = Case(1, 77, 511, 290, fill=[100], softcap=softcap, slopes=slopes, pos=[290], seed=61, qstd=4.0)
+    c.check(*c.run())
+
+
 def test_plain_scores_agree_with_rswa_prefill(cuda_lib):
     c = Case(2, 3, 300, 700, plen=[700, 333], fill=[128, 60], qstd=1.0, seed=53)
     out, lse = c.run()

@@ -116,7 +116,8 @@ RSWA_API size_t rswa_workspace_bytes(const rswa_dims* dims, int32_t op);
  * RSWA_ERR_DEVICE_CHECK otherwise, RSWA_ERR_CUDA if the copy failed.
  * If RSWA_DEVICE_WAIT_TIMEOUT is set, CTAs that gave up may have left completion
  * counters behind, so all ws_bytes of the workspace are zero-filled again (its
- * initial state) and it can be reused; otherwise only the status word is cleared.
+ * initial state) and it can be reused; otherwise only the status word is cleared. Until
+ * then a call on that workspace may leave its output unwritten or wrong.
  * Also accepts the `status` pointer given to rswa_append (ws_bytes >= 4).
  */
 RSWA_API rswa_status rswa_check_status(void* workspace, size_t ws_bytes, int32_t* device_status, void* stream);
@@ -128,7 +129,8 @@ RSWA_API rswa_status rswa_check_status(void* workspace, size_t ws_bytes, int32_t
  * in flight land (bounded by the same limit) and ends the CTA, so the call returns and
  * the CUDA context stays usable. This call arms, for the NEXT decode-family call made
  * by the calling host thread only (rswa_decode*, srswa_decode*, srswa_prefill,
- * rswa_decode_noalloc; of rswa_decode_shared, its private part; consumed by that call even if it fails validation):
+ * rswa_decode_noalloc; of rswa_decode_shared, its private part; consumed by that call even
+ * if it fails validation):
  *   drop_tile     : >= 0: CTA 0 neither arms nor fills the shared-memory stage of its
  *                   CTA-local tile number drop_tile, so that tile's bounded wait runs
  *                   out (no copy is in flight for it); -1: nothing dropped.
@@ -569,8 +571,8 @@ RSWA_API rswa_status srswa_step_rope(const rswa_dims* dims, const rswa_rope* rop
  *                overlap one another.
  *   inv_freq : HOST array f64 [rot_dim / 2], finite, read during the call only
  *   pos      : int32 [batch][tokens], any values
- *   q_out / k_out may be q / k with the same strides (in place; dims from rot_dim on are then
- *   not touched); other overlaps of an output with an input are not supported.
+ *   q_out / k_out may be q / k with the same strides (in place; dims from rot_dim on then keep
+ *   their values); other overlaps of an output with an input are not supported.
  * Arithmetic: the angle as a 64-bit fixed-point fraction of a turn (error below 2^-31 max(1, |inv_freq|) turns
  * for every int32 position), cos / sin and the rotation in f32, one rounding to bf16: within
  * 2^-20 (|x| + |y|) |mscale| plus half a bf16 step of the exact rotation by the table's angles.
@@ -649,8 +651,9 @@ RSWA_API rswa_status rswa_prefill_scored(const rswa_dims* dims, const rswa_score
  * R-SWA decode of sequences that share prefixes: sequence b attends to the rows
  * [0, shared_len[p]) of shared prefix p = share_of[b] (none if -1), to its private prefix rows
  * [0, prefix_len[b]) and to its ring's valid slots, in one softmax. Every shared row is read once
- * for up to 256 sequences (three launches: grouping, the shared part on the tensor cores with the
- * weights rounded to bf16, the private part in f32 joined with it).
+ * for up to 256 sequences (two launches: the shared part on the tensor cores with the weights rounded
+ * to bf16, the private part in f32 joined with it; above 384 sequences or prefixes a launch before
+ * them groups the sequences).
  *   dims       : as rswa_decode; prefix_cap is the PRIVATE capacity and may be 0 (pk, pv and
  *                prefix_len are then not read and may be NULL)
  *   n_shared   : prefixes P, 1..8192;  shared_cap : rows allocated for each, 1..2^30

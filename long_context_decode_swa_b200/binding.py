@@ -969,7 +969,7 @@ def rswa_decode_scored(q, pk, pv, prefix_len, ring_k, ring_v, wp, fill, out, wor
     """R-SWA decode whose scores are softcap * tanh(scale q.k / softcap) (softcap > 0) minus
     slopes[h] * (pos - key position), over prefix rows ranges[b] = (lo, hi) and the ring. q bf16
     [B][H][D]; slopes f32 [H] with pos int32 [B]; ranges int32 [B][2]; out f32 [B][H][D], lse f32
-    [B][H]. workspace: new_workspace(dims, OP_DECODE_SCORED)."""
+    [B][H]. pos is read with slopes only. workspace: new_workspace(dims, OP_DECODE_SCORED)."""
     dev = _device_of(q, "q")
     if q.dim() != 3 or not isinstance(pk, torch.Tensor) or pk.dim() != 4:
         raise ValueError("expected q [B, H, D] and pk [B, H, cap, D]")

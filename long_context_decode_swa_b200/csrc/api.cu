@@ -1073,6 +1073,13 @@ rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_freq, const 
         return fail(RSWA_ERR_INVALID, "%s: rows of %s overlap (a stride of 0)", fn, names[i]);
     }
   }
+  for (int i = 0; i < (d.heads_k > 0 ? 4 : 2); i += 2) {
+    if ((i == 0 ? q : k) != (i == 0 ? q_out : k_out)) continue;
+    const int32_t extent[3] = {d.batch, i == 0 ? d.heads_q : d.heads_k, d.tokens};
+    for (int j = 0; j < 3; ++j)
+      if (extent[j] > 1 && all[i][j] != all[i + 1][j])
+        return fail(RSWA_ERR_INVALID, "%s: %s in place needs the input's strides", fn, names[i + 1]);
+  }
   rswa::Rope1dLaunch L;
   L.B = d.batch;
   L.Hq = d.heads_q;

@@ -32,9 +32,13 @@ constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileBytes = kBlock * kRowBytes;  // 8 KiB
 constexpr int kCtasPerSm = 2;                   // by shared memory
-constexpr int kSoloItems = 4;
-constexpr int kWholeItems = 3;
-constexpr int kWholeRounds = 3;
+// The thresholds of the cut (where it is made says what they mean), with what the values beside
+// them measured, in us:
+constexpr int kSoloItems = 4;    // 1: 144 instead of 134 at 256 x 16 items of 416 rows; 16: 324 instead of 311 with 512 x 16
+                                 // items of 128 rows over shared prefixes (but 184 instead of 190 at 512 x 16 of 288)
+constexpr int kWholeItems = 3;   // 1: 64 instead of 55 at 37 x 12 ragged items of up to 2,099 rows; 12: 44 instead of 40 at
+                                 // 64 x 16 items of 416 rows
+constexpr int kWholeRounds = 3;  // 1: 9.9 instead of 8.0 at 16 items of 416 rows; 9: as 3
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

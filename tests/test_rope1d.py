@@ -46,6 +46,8 @@ def _call(desc=None, freq="ok", pos=A, q=A, q_out=A, k=A, k_out=A):
     (dict(k_out_stride=(2048, 1020, 128)), INVALID, "strides of k_out"),
     (dict(q_out_stride=(4096, 0, 128)), INVALID, "overlap"),
     (dict(dtype=1, q_stride=(4096, 1024, 126)), INVALID, "strides of q "),
+    (dict(q_out_stride=(4096, 2048, 256)), INVALID, "q_out in place"),  # q and q_out are one address here
+    (dict(k_stride=(2048, 128, 256)), INVALID, "k_out in place"),
 ])
 def test_descriptor_refusals(kw, code, word):
     got, msg = _call(_desc(**kw))

@@ -74,7 +74,7 @@ struct __align__(1024) Smem {
   uint64_t q_full;
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_ready[kVStages], v_empty[kVStages];
-  uint64_t s_full[kQTiles], p_full[kQTiles], o_done[kQTiles];
+  uint64_t s_full[kQTiles], p_full[kQTiles][2], o_done[kQTiles];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -101,6 +101,7 @@ struct Args {
   const float* slopes;    // [H], with pos [B], or null
   const int32_t* pos;
   float softcap, scale;
+  float small_u;          // |u| up to which the short polynomial is taken (negative: never)
   int cluster;            // split: CTAs that share a query tile's key tiles
   int first;              // split: the first pair of query tiles that is this launch's
   int late;               // the launch before this one is its own first part: waited for at the end
@@ -194,15 +195,31 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 
+// 2^z of a pair without the special-function unit: z to the nearest integer (the low bits of z + 1.5 2^23) and a
+// rest f in [-1/2, 1/2], 2^f as a minimax polynomial of degree 4 (relative error 2.6e-6, a 700th of the
+// rounding to bf16 that follows), the integer added to its exponent. z <= 2^8; below -126: 2^-126.
+__device__ __forceinline__ float2 ex2_pair(float2 z) {
+  z = make_float2(fmaxf(z.x, -126.f), fmaxf(z.y, -126.f));
+  const float2 t = __fadd2_rn(z, splat(12582912.f));
+  const float2 n = __fadd2_rn(t, splat(-12582912.f));
+  const float2 f = __ffma2_rn(n, splat(-1.f), z);
+  float2 p = __ffma2_rn(splat(0.00957009898f), f, splat(0.0559178601f));
+  p = __ffma2_rn(p, f, splat(0.240247449f));
+  p = __ffma2_rn(p, f, splat(0.693121815f));
+  p = __ffma2_rn(p, f, splat(0.999999261f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+// Of plain scores' exponentials every kPolyPairs-th pair goes there: with one in four 16 heads x 2304 queries
+// x 10272 rows take 185 us instead of 188, and x 1152 queries 102 instead of 108. (Capped ones keep the FMA pipe busy.)
+constexpr int kPolyPairs = 4;
+
 // tanh(u) = u p(u^2): minimax polynomials, within 2e-8 for |u| up to 0.4 and up to 1 (four and seven terms).
 constexpr float kTanhSmall = 0.4f, kTanhMid = 1.f;
-struct TanhSmall {
-  static constexpr int kTerms = 4;
-  static __device__ __forceinline__ float coef(int i) {
-    constexpr float c[kTerms] = {0.999999573f, -0.333297261f, 0.132505672f, -0.0468257397f};
-    return c[i];
-  }
-};
+__host__ __device__ constexpr float tanh_small_coef(int i) {
+  constexpr float c[4] = {0.999999573f, -0.333297261f, 0.132505672f, -0.0468257397f};
+  return c[i];
+}
 struct TanhMid {
   static constexpr int kTerms = 7;
   static __device__ __forceinline__ float coef(int i) {
@@ -211,6 +228,32 @@ struct TanhMid {
     return c[i];
   }
 };
+
+// The short polynomial with the scores' factors in its coefficients: cap2 tanh(raw k) = raw q(raw^2),
+// q_i = c_i cap2 k^(2 i + 1). A multiplication less a pair (889 -> 865 us at 2 x 16 heads x 4096 queries x
+// 10272 rows, capped); taken where the coefficients stay well inside the f32 range (Args.small_u).
+struct TanhFolded {
+  float q[4];
+};
+
+__device__ __forceinline__ TanhFolded fold_tanh(float k, float cap2) {
+  TanhFolded t;
+  float f = cap2 * k;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t.q[i] = tanh_small_coef(i) * f;
+    f *= k * k;
+  }
+  return t;
+}
+
+__device__ __forceinline__ float2 capped_pair(float2 raw, const TanhFolded& t, float2 add) {
+  const float2 w = __fmul2_rn(raw, raw);
+  float2 p = __ffma2_rn(splat(t.q[3]), w, splat(t.q[2]));
+  p = __ffma2_rn(p, w, splat(t.q[1]));
+  p = __ffma2_rn(p, w, splat(t.q[0]));
+  return __ffma2_rn(raw, p, add);
+}
 
 // cap2 tanh(raw k) + add, for a pair.
 template <typename Poly>
@@ -271,9 +314,9 @@ __device__ __forceinline__ RowTile row_tile(const Ctx& c, int kind, int start, i
 // How a warp takes the tanh of some scores: by the largest |u| among its rows'.
 enum Tanh { kSmall, kMid, kExact };
 
-__device__ __forceinline__ Tanh tanh_of(float lowest, float highest, float k) {
+__device__ __forceinline__ Tanh tanh_of(float lowest, float highest, float k, float small_u) {
   const float u = fmaxf(highest, -lowest) * k;
-  if (__all_sync(0xffffffffu, u <= kTanhSmall)) return kSmall;
+  if (__all_sync(0xffffffffu, u <= small_u)) return kSmall;
   return __all_sync(0xffffffffu, u <= kTanhMid) ? kMid : kExact;
 }
 
@@ -301,14 +344,14 @@ __device__ __forceinline__ float lowest_of(const float (&x)[32], float a) {
 // k: scale / cap, or scale log2(e) without a cap; full (uniform over the warp): nothing is masked.
 template <bool kCap, bool kBias>
 __device__ __forceinline__ void score_chunk(float (&x)[32], const RowTile& t, int col0, bool full, float k, float cap2,
-                                            float slope2, int n) {
+                                            float small_u, float slope2, int n) {
   // -slope (base - e) = slope e + c0: exact integers, one rounding of the bias
   const float c0 = kBias ? -slope2 * (float)(t.base - col0) : 0.f;
   auto bias = [&](int e) {
     // (not paired: a pair of constants would take two moves, one is an immediate operand)
     return kBias ? make_float2(fmaf(slope2, (float)e, c0), fmaf(slope2, (float)(e + 1), c0)) : make_float2(0.f, 0.f);
   };
-  const Tanh how = kCap ? tanh_of(lowest_of(x, INFINITY), highest_of(x, -INFINITY), k) : kSmall;
+  const Tanh how = kCap ? tanh_of(lowest_of(x, INFINITY), highest_of(x, -INFINITY), k, small_u) : kSmall;
   if (kCap && how == kExact) {
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
@@ -324,11 +367,12 @@ __device__ __forceinline__ void score_chunk(float (&x)[32], const RowTile& t, in
       x[e + 1] = s2.y;
     }
   } else {
+    const TanhFolded folded = fold_tanh(k, cap2);  // (without a cap not used)
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
       float2 s2 = make_float2(x[e], x[e + 1]);
       if (kCap)
-        s2 = capped_pair<TanhSmall>(s2, k, cap2, bias(e));
+        s2 = capped_pair(s2, folded, bias(e));
       else
         s2 = kBias ? __ffma2_rn(s2, splat(k), bias(e)) : __fmul2_rn(s2, splat(k));
       x[e] = s2.x;
@@ -387,22 +431,22 @@ __device__ __forceinline__ uint4 to_bf16x8(const float* o) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The 256 threads of a stream meet (barrier 1 + x); whether any of them says so.
-__device__ __forceinline__ bool stream_any(int x, bool v) {
+// The two warps that share 32 rows of a stream meet (barrier 1 + pair); whether any thread of them says so.
+__device__ __forceinline__ bool pair_any(int pair, bool v) {
   uint32_t any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 256, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(any)
-      : "r"(v ? 1u : 0u), "r"(1 + x)
+      : "r"(v ? 1u : 0u), "r"(1 + pair)
       : "memory");
   return any != 0;
 }
-__device__ __forceinline__ void stream_barrier(int x) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + x) : "memory"); }
+__device__ __forceinline__ void stream_barrier(int x) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(9 + x) : "memory"); }
 // Both streams meet.
-__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 3, 512;" ::: "memory"); }
+__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 11, 512;" ::: "memory"); }
 
 template <bool kCap, bool kBias, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -413,6 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   constexpr int kCtaRows = kSplit ? kRows : kMaxRows;
+  // P goes to the MMAs in two parts, so that the first 64 keys' products run under the exponentials of the
+  // others: 202 -> 196 us at 16 heads x 2304 queries x 10272 rows of plain scores; capped ones without a bias,
+  // whose exponentials wait on the FMA pipe, took 879 us whole and 889 in parts (2 x 16 heads x 4096 queries).
+  constexpr bool kInParts = !kCap || kBias;
   const int cluster = kSplit ? a.cluster : 1;
   const int rank = kSplit ? (int)cluster_rank() : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -449,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int x = 0; x < kQTiles; ++x) {
       mbar_init(&sm.s_full[x], 1);
-      mbar_init(&sm.p_full[x], 8);  // one arrival a warp
+      for (int u = 0; u < 2; ++u) mbar_init(&sm.p_full[x][u], 8);  // one arrival a warp
       mbar_init(&sm.o_done[x], 1);
     }
     mbar_init(&sm.drain, 1);
@@ -633,13 +681,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_commit(&sm.s_full[x]);
         };
-        auto issue_pv = [&](int x, int vs, bool more) {  // O_x += P_x V
+        auto issue_pv = [&](int x, int vs, uint32_t phase, bool more) {  // O_x += P_x V, P in two parts as it comes
           const uint64_t v = v_desc + (uint64_t)(vs * (kTileBytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int e = 0; e < 8; ++e) {
+            const int kk = (e & 1) + (e >> 1 & 1) * 4 + (e >> 2) * 2;  // both halves' first 32 columns, then their last
+            if (e == 0 || (kInParts && e == 4)) {
+              if (!wait_or_abort(sm, &sm.p_full[x][kInParts ? e / 4 : 1], phase, a.status)) return false;
+              tc_fence_after();
+            }
             tc_mma_ts(tmem + kColO + (uint32_t)x * 128u, tmem + (uint32_t)x * 128u + (uint32_t)((kk >> 2) * kHalf + (kk & 3) * 8),
-                      v + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (more || kk > 0) ? 1u : 0u);
+                      v + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (more || e > 0) ? 1u : 0u);
+          }
           tc_commit(&sm.o_done[x]);
+          return true;
         };
         bool ok = wait_or_abort(sm, &sm.q_full, 0, a.status);
         uint32_t p_phase[kQTiles] = {0, 0};
@@ -675,9 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a.status))) break;
           if (kSplit) {
             const int x = t & 1;
-            if (!(ok = wait_or_abort(sm, &sm.p_full[x], (t >> 1) & 1, a.status))) break;
-            tc_fence_after();
-            issue_pv(x, vs, t > 1);
+            if (!(ok = issue_pv(x, vs, (t >> 1) & 1, t > 1))) break;
             tc_commit(&sm.v_empty[vs]);
             if (t + 2 < total) {
               if (!(ok = take_k(seen))) break;
@@ -689,10 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < kQTiles; ++x) {
               if (seen >> x & 1) {
-                if (!(ok = wait_or_abort(sm, &sm.p_full[x], p_phase[x], a.status))) break;
+                if (!(ok = issue_pv(x, vs, p_phase[x], more[x]))) break;
                 p_phase[x] ^= 1;
-                tc_fence_after();
-                issue_pv(x, vs, more[x]);
                 more[x] = true;
               }
               if (x == 0 && next && !(ok = take_k(seen_next))) break;
@@ -777,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (kSplit ? 0 : x * kRows) + r;  // row of the CTA
     const int i = c.i0 + row;
     const int col0 = half * kHalf;
+    const int rows32 = 4 * x + (sw & 3);  // its 32 rows of the CTA's, which one other warp has too
     const uint32_t lane_base = (uint32_t)((sw & 3) * 32) << 16;
     const uint32_t s_cols = tmem + lane_base + (uint32_t)(x * 128 + col0);  // its scores; its P goes over their first half
     const uint32_t o_cols = tmem + lane_base + kColO;                       // O of stream A; B's is 128 columns on
@@ -840,11 +892,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             highest = highest_of(v, highest);
             if (kCap) lowest = lowest_of(v, lowest);
           }
-          if (kCap) how = tanh_of(lowest, highest, mul);
+          if (kCap) how = tanh_of(lowest, highest, mul, a.small_u);
           // without a mask the raw maximum gives the maximum (a bound of it, where a bias is added), and the
           // scoring joins the exponentials' loop
           fused = !kCap || how != kExact;
-          tmax = kCap ? cap2 * tanhf(highest * mul) : highest * mul;
+          if (!kCap)
+            tmax = highest * mul;
+          else if (how == kSmall)
+            tmax = capped_pair(splat(highest), fold_tanh(mul, cap2), splat(0.f)).x;
+          else if (how == kMid)
+            tmax = capped_pair<TanhMid>(splat(highest), mul, cap2, splat(0.f)).x;
           if (kBias) tmax += fmaf(fmaxf(slope2, 0.f), (float)(kHalf - 1), -slope2 * (float)(rt.base - col0));
         }
         if (!fused) {
@@ -853,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int ch = 0; ch < 2; ++ch) {
             float v[32];
             load(ch, v);
-            score_chunk<kCap, kBias>(v, rt, col0 + ch * 32, full, mul, cap2, slope2, c.n);
+            score_chunk<kCap, kBias>(v, rt, col0 + ch * 32, full, mul, cap2, a.small_u, slope2, c.n);
             tmax = highest_of(v, tmax);
             uint32_t w[32];
 #pragma unroll
@@ -863,11 +920,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
         }
       }
-      // Both halves of the stream meet here, also after a give-up. The running maximum only moves when
+      // Both warps of the rows meet here, also after a give-up. The running maximum only moves when
       // it grows by more than 2^8 (the exponentials stay below 256): then the halves agree on it.
-      if (stream_any(x, !ok || tmax > m_used + kLazyRescaleLog2)) {
+      if (pair_any(rows32, !ok || tmax > m_used + kLazyRescaleLog2)) {
         sm.half[x][half][r] = tmax;
-        if (stream_any(x, !ok)) {
+        if (pair_any(rows32, !ok)) {
           ok = false;
           break;
         }
@@ -892,10 +949,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      auto given = [&](int part) {  // of P
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[x][part]);
+      };
       if (none) {
         const uint32_t zero[16] = {};
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) tmem_st16(s_cols + (uint32_t)ch * 16u, zero);
+        if (kInParts) given(0);
       } else {
         const float2 minus_m = splat(m_used == -INFINITY ? 0.f : -m_used);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
@@ -910,7 +974,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) {
               const float2 add = kBias && !kSplit && fused ? make_float2(fmaf(slope2, (float)(2 * e), c0), fmaf(slope2, (float)(2 * e + 1), c0)) : minus_m;
               const float2 z2 = less_m(make_float2(v[2 * e], v[2 * e + 1]), add);
-              const float2 p2 = make_float2(ex2(z2.x), ex2(z2.y));
+              const bool poly = !kCap && !kBias && e % kPolyPairs == 1;
+              const float2 p2 = poly && fused ? ex2_pair(z2) : make_float2(ex2(z2.x), ex2(z2.y));
               const __nv_bfloat162 pb = __floats2bfloat162_rn(p2.x, p2.y);
               pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
               if (e & 1)
@@ -919,6 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum0 = __fadd2_rn(sum0, p2);
             }
             tmem_st16(s_cols + (uint32_t)ch * 16u, pk);
+            if (kInParts && ch == 0) given(0);
           }
         };
         if (!fused)  // (a split biased chunk's only way)
@@ -926,15 +992,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (!kCap)
           weights([&](float2 z, float2 add) { return __ffma2_rn(z, splat(mul), add); });
         else if (how == kSmall)
-          weights([&](float2 z, float2 add) { return capped_pair<TanhSmall>(z, mul, cap2, add); });
+          weights([&, folded = fold_tanh(mul, cap2)](float2 z, float2 add) { return capped_pair(z, folded, add); });
         else
           weights([&](float2 z, float2 add) { return capped_pair<TanhMid>(z, mul, cap2, add); });
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[x]);
+      given(1);
       ++j;
     }
     if (ok && j > 0) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (j - 1) & 1, a.status));
@@ -1113,6 +1176,12 @@ cudaError_t launch_scored_prefill(const ScoredPrefillLaunch& L, cudaStream_t str
   a.pos = L.pos;
   a.softcap = L.softcap;
   a.scale = L.scale;
+  a.small_u = -1.f;
+  if (L.softcap > 0.f) {
+    const double k = (double)L.scale / L.softcap, cap2 = (double)L.softcap * kLog2e;
+    const double least = std::fabs(tanh_small_coef(3)) * cap2 * std::pow(k, 7), most = std::fmax(cap2 * k, cap2 * std::pow(k, 7));
+    if (least > 1e-36 && most < 1e36) a.small_u = kTanhSmall;
+  }
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;
   a.status = L.status;

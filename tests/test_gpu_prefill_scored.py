@@ -25,8 +25,9 @@ def slopes_of(H):
 
 class Case:
     def __init__(self, B, H, T, cap, n=128, plen=None, fill=None, softcap=0.0, slopes=None, pos=None, ranges=None,
-                 qstd=4.0, seed=0):
+                 qstd=4.0, seed=0, scale=None):
         g = P64.gen(3000 + seed)
+        self.scale = scale
         self.B, self.H, self.T, self.cap, self.n, self.softcap = B, H, T, cap, n, softcap
         self.q, self.ko, self.vo = randn((B, H, T, D), g, qstd), randn((B, H, T, D), g), randn((B, H, T, D), g)
         self.plen = ints(plen if plen is not None else [cap] * B)
@@ -47,7 +48,7 @@ class Case:
             stream.wait_stream(torch.cuda.current_stream())
         pkg.rswa_prefill_scored(self.q, self.ko, self.vo, self.pk, self.pv, self.plen, out, self.ws if ws is None else ws,
                                 softcap=self.softcap, slopes=self.slopes, pos=self.pos, ranges=self.ranges, lse=lse,
-                                write_ring=write_ring, stream=stream, **ring)
+                                write_ring=write_ring, stream=stream, scale=self.scale, **ring)
         return out, lse
 
     def check(self, out, lse, rel=5e-3):
@@ -79,7 +80,7 @@ class Case:
                 # rows of the prefix that nobody sees may hold anything
                 dead = ~seen.any(0)
                 k, v = k.masked_fill(dead[:, None], 0.0), v.masked_fill(dead[:, None], 0.0)
-                o, e, size = P64.attend(self.q[b, h].double(), k, v, bias, self.softcap)
+                o, e, size = P64.attend(self.q[b, h].double(), k, v, bias, self.softcap, self.scale)
                 err = (out[b, h] - o).abs()
                 bound = (2 * 2.0 ** -8 + 2e-4) * size + 2.0 ** -8 * o.abs() + 1e-30
                 assert (err <= bound).all(), (b, h, (err - bound).max().item(), torch.nonzero(err > bound)[0].tolist())
@@ -184,6 +185,19 @@ def test_gentle_and_steep_slopes_of_many_queries(cuda_lib, softcap):
     slopes = [0.7, -0.7, 0.34, -0.34, 0.36, -0.36, 0.02, -0.02, 0.0, 4.0, -4.0] * 7
     c = Case(1, 77, 511, 290, fill=[100], softcap=softcap, slopes=slopes, pos=[290], seed=61, qstd=4.0)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("softcap,scale", [(1e-3, None), (0.5, None), (1e6, None), (30.0, 1e-9), (1e-3, 3.0), (1e6, 1e-4)])
+def test_extreme_caps_and_scales(cuda_lib, softcap, scale):
+    # scores far above and far below the cap, and products of the two far from 1
+    c = Case(1, 2, 200, 300, fill=[60], softcap=softcap, seed=62, qstd=1.0, scale=scale)
+    c.check(*c.run())
+
+
+def test_rows_far_below_their_maximum(cuda_lib):
+    # weights from 1 down past the least of f32, in whole tiles
+    c = Case(1, 80, 300, 700, fill=[128], seed=63, qstd=20.0)
+    c.check(*c.run(), rel=8e-3)  # outputs are one row of V: no averaging, rounding alone
 
 
 def test_plain_scores_agree_with_rswa_prefill(cuda_lib):

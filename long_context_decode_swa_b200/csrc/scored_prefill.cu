@@ -847,11 +847,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         ref = max(min(i + c.fill, c.n - 1), pre ? pos - range.x : 0);
     }
-    // Where the bias changes by at most 2^32 along a thread's columns, the largest raw score and the largest
-    // bias bound the row's maximum closely enough: its weights stay above 2^-41, far from fp32's least.
-    // (Paired only: 382 -> 358 us at 16 heads x 2368 queries x 10272 rows; a split chunk of 3 x 333 queries
-    // over documents, where few tiles are seen whole, took 64 us with it and takes 57 without.)
-    const bool gentle = fabsf(slope2) * (float)(kHalf - 1) <= 32.f;
+    // Where the bias changes by at most 2^60 along 32 columns, their largest raw score and their largest bias
+    // bound the row's maximum closely enough: its weights stay above 2^-69, far from f32's least. (Paired only:
+    // 382 -> 358 us at 16 heads x 2368 queries x 10272 rows, capped, by 64 columns and 334 -> 326 later by 32; a split
+    // chunk of 3 x 333 queries over documents, whose tiles wait for the slowest of 8 warps, often a masked one, took
+    // 55 us without it and 59 with.)
+    const bool gentle = fabsf(slope2) * 31.f <= 60.f;
     // l sums the unrounded weights, for O and lse alike: where one key dominates, O is off by the
     // rounding of its weight (at most half a bf16 step, as the output's own rounding); summing the
     // rounded ones too cost three more instructions a score pair
@@ -884,25 +885,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       float tmax = -INFINITY;
       if (ok && !none) {
         if (full && (!kBias || (!kSplit && gentle && rt.cut >= kRows))) {
-          float lowest = INFINITY, highest = -INFINITY;
+          float lowest = INFINITY;
+          float2 top = splat(-INFINITY);  // with a bias of each 32 columns, else of all
 #pragma unroll 1
           for (int ch = 0; ch < 2; ++ch) {
             float v[32];
             load(ch, v);
-            highest = highest_of(v, highest);
+            if (kBias) top.x = top.y;
+            top.y = highest_of(v, kBias ? -INFINITY : top.y);
             if (kCap) lowest = lowest_of(v, lowest);
           }
-          if (kCap) how = tanh_of(lowest, highest, mul, a.small_u);
-          // without a mask the raw maximum gives the maximum (a bound of it, where a bias is added), and the
+          if (!kBias) top.x = top.y;
+          if (kCap) how = tanh_of(lowest, fmaxf(top.x, top.y), mul, a.small_u);
+          // without a mask the raw maxima give the maximum (a bound of it, where a bias is added), and the
           // scoring joins the exponentials' loop
           fused = !kCap || how != kExact;
           if (!kCap)
-            tmax = highest * mul;
+            top = __fmul2_rn(top, splat(mul));
           else if (how == kSmall)
-            tmax = capped_pair(splat(highest), fold_tanh(mul, cap2), splat(0.f)).x;
+            top = capped_pair(top, fold_tanh(mul, cap2), splat(0.f));
           else if (how == kMid)
-            tmax = capped_pair<TanhMid>(splat(highest), mul, cap2, splat(0.f)).x;
-          if (kBias) tmax += fmaf(fmaxf(slope2, 0.f), (float)(kHalf - 1), -slope2 * (float)(rt.base - col0));
+            top = capped_pair<TanhMid>(top, mul, cap2, splat(0.f));
+          if (kBias) {
+            const float b0 = fmaf(fmaxf(slope2, 0.f), 31.f, -slope2 * (float)(rt.base - col0));
+            top = make_float2(top.x + b0, top.y + fmaf(slope2, 32.f, b0));
+          }
+          tmax = fmaxf(top.x, top.y);
         }
         if (!fused) {
           tmax = -INFINITY;

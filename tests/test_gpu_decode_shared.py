@@ -113,6 +113,25 @@ def test_many_prefixes(cuda_lib):
     c.check(*c.run())
 
 
+def test_the_most_prefixes(cuda_lib):
+    c = Case(70, 8192, 1, 2, n=2, share=[(b * 117) % 8192 for b in range(69)] + [8191], seed=14)
+    c.check(*c.run())
+
+
+def test_one_workspace_for_calls_of_many_sizes(cuda_lib):
+    # tables, records and counters of one call lie where the next one's do, or elsewhere
+    cases = [Case(3, 1, 2, 300, n=5, seed=15), Case(420, 7, 1, 200, cap=9, seed=16), Case(40, 3, 4, 4000, seed=17),
+             Case(1, 1, 1, 1, n=1, seed=18), Case(257, 1, 1, 129, seed=19)]
+    ws = max((c.ws for c in cases), key=lambda w: w.numel())
+    refs = [c.run() for c in cases]
+    got = [c.run(ws=ws) for c in cases + cases[::-1]]
+    for (o, e), (ro, re) in zip(got, refs + refs[::-1]):
+        assert torch.equal(o, ro) and torch.equal(e, re)
+    for c, r in zip(cases, refs):
+        c.check(*r)
+    assert pkg.check_status(ws) == 0
+
+
 def test_one_peaked_key_and_large_scores(cuda_lib):
     # one key far above the rest, first in a late tile: the running maximum moves by hundreds
     c = Case(9, 1, 2, 900, seed=8)

@@ -19,9 +19,12 @@
 // rows of a tile that no query of the CTA sees are zeroed in V (0 * NaN would reach O). A chunk over
 // packed documents so costs what its documents cost, not what the prefix does.
 //
-// Scores: the special-function unit (16 a cycle and SM) bounds the kernel: one ex2 a score is 1,024
-// cycles a tile, as many as its MMAs take. tanh(u) = 1 - 2 / (e^2u + 1) would cost two more; where a warp's
-// scores all have |u| = |scale q.k| / cap <= 0.4 (or 1), tanh is u times a minimax polynomial in u^2
+// What bounds it: a tile's MMAs take 1,024 cycles, and one ex2 a score as many of the special-function
+// unit (16 a cycle and SM); a stream's chain of scores, maximum, exponentials and P V takes some 5,000, of which
+// the two streams' overlap leaves the tensor pipe 40 to 49% busy. 2 x 16 heads x 4096 capped queries over 10272
+// rows take 870 to 890 us (430 at the measured tensor rate) and run into the power limit there (820 in a burst).
+//
+// Scores: tanh(u) = 1 - 2 / (e^2u + 1) would cost two more special-function operations; where a warp's scores all have |u| = |scale q.k| / cap <= 0.4 (or 1), tanh is u times a minimax polynomial in u^2
 // instead, on the packed FMA pipe (errors below 1e-7 of the cap either way).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -897,7 +900,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool full = __all_sync(0xffffffffu, rt.lo <= col0 && rt.hi >= to);
       // The passes over the row's scores go 32 columns at a time, through TMEM, in loops that are not
       // unrolled: holding all of them in registers made straight-line code of 20 to 40 KB a tile, which
-      // the instruction cache did not feed (a biased tile took 8,000 cycles instead of 4,000).
+      // the instruction cache did not feed (a biased tile took 8,000 cycles instead of 4,000). 16 columns at
+      // a time took 236 us where this takes 224 (16 heads x 2304 capped queries x 10272 rows).
       auto load = [&](int ch, float(&v)[32]) {
         uint32_t raw[32];
         tmem_ld32(s_cols + (uint32_t)ch * 32u, raw);

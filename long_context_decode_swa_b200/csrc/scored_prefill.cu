@@ -24,7 +24,8 @@
 // the two streams' overlap leaves the tensor pipe 40 to 49% busy. 2 x 16 heads x 4096 capped queries over 10272
 // rows take 870 to 890 us (430 at the measured tensor rate) and run into the power limit there (820 in a burst).
 //
-// Scores: tanh(u) = 1 - 2 / (e^2u + 1) would cost two more special-function operations; where a warp's scores all have |u| = |scale q.k| / cap <= 0.4 (or 1), tanh is u times a minimax polynomial in u^2
+// Scores: tanh(u) = 1 - 2 / (e^2u + 1) would cost two more special-function operations; where a warp's
+// scores all have |u| = |scale q.k| / cap <= 0.4 (or 1), tanh is u times a minimax polynomial in u^2
 // instead, on the packed FMA pipe (errors below 1e-7 of the cap either way).
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -223,6 +223,8 @@ def _device_of(t, name: str) -> int:
 # The raw handle of a device's current stream, without building a torch.cuda.Stream (2 us a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The current device without torch.cuda.current_device's check that CUDA is initialised (a CUDA tensor exists here).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _fns: dict = {}
 
 
@@ -235,7 +237,7 @@ def _call(name: str, index: int, stream, *args):
         raw = _raw_stream(index)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         code = fn(*args, raw)
     else:
         with torch.cuda.device(index):

@@ -200,6 +200,18 @@ def test_rows_far_below_their_maximum(cuda_lib):
     c.check(*c.run(), rel=8e-3)  # outputs are one row of V: no averaging, rounding alone
 
 
+@pytest.mark.parametrize("softcap,bias,B,H", [(0.0, False, 1, 8), (20.0, False, 1, 8), (0.0, True, 1, 8), (20.0, True, 1, 8),
+                                              (0.0, False, 2, 80)])
+def test_a_nan_key_that_is_seen_shows(cuda_lib, softcap, bias, B, H):
+    # one key of each head, in each place of eight: no query's output hides it
+    c = Case(B, H, 150, 400, fill=[128] * B, softcap=softcap, slopes=slopes_of(H) if bias else None,
+             pos=[400] * B if bias else None, seed=64)
+    for h in range(H):
+        c.pk[:, h, 128 + h % 8, 5] = math.nan
+    out, lse = c.run()
+    assert not torch.isfinite(out).any() and not torch.isfinite(lse).any()
+
+
 def test_plain_scores_agree_with_rswa_prefill(cuda_lib):
     c = Case(2, 3, 300, 700, plen=[700, 333], fill=[128, 60], qstd=1.0, seed=53)
     out, lse = c.run()

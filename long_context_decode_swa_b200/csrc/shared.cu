@@ -726,7 +726,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the segment's records ----
       const bool any = x < events;
       if (ok && any) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (seen - 1) & 1, a.status));
-      if (!two) {
+      // Group B without a score of its own writes nothing: it has waited for nothing in this segment, and group A
+      // may still be reading the statistics of the segment before. (A group with a score has waited for scores,
+      // which were issued when all threads of both groups had brought this segment's queries, past their reads.)
+      if (!two && any) {
         sm.stat_m[x][r] = m_used;
         if (x == 1) {
           sm.stat_l[r] = l;
@@ -758,12 +761,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // the two groups' halves of the keys meet; each writes half of the columns
           const bool both = events > 1;
-          const float ma = sm.stat_m[0][r], mb = sm.stat_m[1][r];
+          const float ma = sm.stat_m[0][r], mb = both ? sm.stat_m[1][r] : -INFINITY;
           const float M = fmaxf(ma, mb), m_sub = M == -INFINITY ? 0.f : M;
           const float fa = ex2(ma - m_sub), fb = both ? ex2(mb - m_sub) : 0.f;
           if (live && x == 0)
-            *reinterpret_cast<float4*>(rec) =
-                make_float4(M, fmaf(sm.stat_l[r], fb, l * fa), fmaf(sm.stat_lu[r], fb, lu * fa), 0.f);
+            *reinterpret_cast<float4*>(rec) = make_float4(M, both ? fmaf(sm.stat_l[r], fb, l * fa) : l * fa,
+                                                          both ? fmaf(sm.stat_lu[r], fb, lu * fa) : lu * fa, 0.f);
 #pragma unroll 1
           for (int ch = 0; ch < 2; ++ch) {
             const uint32_t col = (uint32_t)(x * 64 + ch * 32);

@@ -220,3 +220,20 @@ def test_binding_refusals(cuda_lib):
                     (dict(lse=lse[:, :1]), ValueError), (dict(q=c.q.transpose(0, 1)), ValueError)]:
         with pytest.raises(err):
             pkg.rswa_decode_shared(**{**base, **kw})
+
+
+@pytest.mark.parametrize("B,P,H,scap", [
+    (40, 16, 12, 300),   # 576 key tiles, four a CTA: three and one, two and two, one and three
+    (24, 24, 37, 250),   # 1,776 key tiles, twelve a CTA: six segments of two each
+    (64, 64, 37, 100),   # sixteen segments of one tile a CTA
+    (31, 31, 43, 140),   # 2,666 key tiles, nineteen a CTA: two and one, in turn about the cuts
+])
+def test_segments_of_one_key_tile_after_others(cuda_lib, B, P, H, scap):
+    # at most 128 readers: a segment of one key tile leaves the second group of rows without a score, right
+    # after a segment whose sums the groups told each other
+    c = Case(B, P, H, scap, n=8, seed=2000 + scap)
+    ref = c.run()
+    c.check(*ref)
+    for _ in range(20):
+        out, lse = c.run()
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])

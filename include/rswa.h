@@ -610,7 +610,8 @@ RSWA_API rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_fre
  *     range   : int32 [batch][2] device array (8-byte aligned): lo, hi; lo >= hi: no prefix row;
  *               not within [0, prefix_len[b]]: flagged RSWA_DEVICE_BAD_RANGE, no prefix row; or
  *               NULL: the whole prefix
- * A query that sees no row at all has out 0 and lse -inf. Rows outside the range are not read.
+ * A query that sees no row at all, or only scores of -inf, has out 0 and lse -inf. Rows outside the range
+ * are not read.
  * The distance bias is taken relative to the query's most favoured row, in integers, so far
  * documents lose no precision. prefix_cap may be 0 (pk, pv, prefix_len are then not read).
  */

@@ -207,9 +207,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // 2^z of a pair without the special-function unit: z to the nearest integer (the low bits of z + 1.5 2^23) and a
 // rest f in [-1/2, 1/2], 2^f as a minimax polynomial of degree 4 (relative error 2.6e-6, a 700th of the
-// rounding to bf16 that follows), times 2 to the integer. z <= 2^8; below -126: 2^-126; NaN: NaN.
+// rounding to bf16 that follows), times 2 to the integer. z <= 2^8; NaN: NaN. An integer of -127 has the bits of
+// 0 as its power: z below -126.5, -inf too, gives 0 (as ex2 with flush-to-zero does below -126).
 __device__ __forceinline__ float2 ex2_pair(float2 z) {
-  z = make_float2(max_nan(z.x, -126.f), max_nan(z.y, -126.f));
+  z = make_float2(max_nan(z.x, -127.f), max_nan(z.y, -127.f));
   const float2 t = __fadd2_rn(z, splat(12582912.f));
   const float2 n = __fadd2_rn(t, splat(-12582912.f));
   const float2 f = __ffma2_rn(n, splat(-1.f), z);

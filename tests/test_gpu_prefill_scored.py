@@ -307,3 +307,38 @@ def test_binding_refusals(cuda_lib):
                     (dict(lse=lse[0]), ValueError), (dict(scale=math.inf), pkg.RswaError)]:
         with pytest.raises(err):
             pkg.rswa_prefill_scored(**{**base, **kw})
+
+
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), (0.0, True), (20.0, False), (20.0, True)])
+@pytest.mark.parametrize("H,T,cap", [(80, 300, 400), (4, 300, 400), (2, 40, 1500)])
+def test_scores_of_minus_infinity(cuda_lib, H, T, cap, softcap, bias):
+    # every key of the even heads scores -inf: without a cap such a query has no weight to give, like one that
+    # sees no row (out 0, lse -inf), in whole tiles as in masked ones; with a cap every score is -cap. Odd heads
+    # are what they are without such neighbours.
+    c = Case(1, H, T, cap, fill=[128], softcap=softcap, slopes=[0.0] * H if bias else None, pos=[cap] if bias else None,
+             seed=65, qstd=1.0)
+    before = c.run()
+    c.q[..., 0] = c.q[..., 0].abs() + 1.0
+    after = c.run()
+    for k in (c.pk, c.ko, c.rk):
+        k[:, ::2, :, 0] = -math.inf
+    out, lse = c.run()
+    assert not torch.equal(before[0], after[0])
+    o, o0, e, e0 = (t[:, 1::2].double() for t in (out, after[0], lse, after[1]))
+    if softcap == 0.0:
+        assert torch.equal(o, o0) and torch.equal(e, e0)
+    else:
+        # a warp's form of the tanh goes by all scores of its 32 columns, and a head's last key tile runs into the
+        # next head's rows: any form's score is within 7e-7 cap (1.4e-5), so two runs' lse within 2.8e-5 and a last
+        # rounding, and weights within 5.6e-5 of each other, each then rounded to bf16, as the outputs are
+        assert (e - e0).abs().max().item() <= 4e-5
+        most = max(t.float().nan_to_num(0.0).abs().max().item() for t in (c.pv, c.vo, c.rv))
+        assert ((o - o0).abs() <= (2 * 2.0 ** -8 + 6e-5) * most + 2 * 2.0 ** -8 * o0.abs()).all()
+        assert (o - o0).norm() <= 5e-3 * o0.norm()
+    if softcap == 0.0:
+        assert (out[:, ::2] == 0).all() and torch.isneginf(lse[:, ::2]).all()
+    else:
+        seen = cap + torch.clamp(128 - 1 - torch.arange(T, device="cuda"), min=0) + torch.clamp(torch.arange(T, device="cuda") + 1, max=128)
+        ref = seen.double().log() - softcap
+        assert (lse[:, ::2].double() - ref).abs().max().item() <= 1e-4
+    assert pkg.check_status(c.ws) == 0

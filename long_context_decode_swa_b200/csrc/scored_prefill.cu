@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               issue_s(t, ks);
               free_k();
             }
-        } else if (ok && (ok = take_k(seen))) {
+        } else if (ok && total > 0 && (ok = take_k(seen))) {  // (no tile: a CTA after a give-up)
           if (seen & 1) issue_s(0, ks);
           if (seen & 2) issue_s(1, ks);
           free_k();

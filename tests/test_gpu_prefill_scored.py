@@ -7,6 +7,7 @@ for the capped form at cap 50, and 2^-23 of a bias that matters. Over a tensor t
 roundings have a relative 2-norm near sqrt(2) 2^-8 / sqrt(3) = 3.2e-3: 5e-3 is asserted where rows
 average over many keys. lse comes from unrounded weights: 1e-4."""
 import math
+import time
 
 import pytest
 import torch
@@ -342,3 +343,22 @@ def test_scores_of_minus_infinity(cuda_lib, H, T, cap, softcap, bias):
         ref = seen.double().log() - softcap
         assert (lse[:, ::2].double() - ref).abs().max().item() <= 1e-4
     assert pkg.check_status(c.ws) == 0
+
+
+@pytest.mark.parametrize("B,H,T", [(2, 80, 600), (2, 8, 300)])
+def test_a_workspace_that_says_timeout_costs_no_waits(cuda_lib, B, H, T):
+    # three waves of paired query tiles and a split rest, or split tiles alone, on a workspace whose status word
+    # already holds a give-up: the CTAs do no work and wait for nothing, the flag stays until it is read, and then
+    # the workspace serves as before
+    c = Case(B, H, T, 300, fill=[128] * B, softcap=20.0, seed=66)
+    ref = c.run()
+    c.ws.view(torch.int32)[0] = bind.DEVICE_WAIT_TIMEOUT
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    c.run()
+    torch.cuda.synchronize()
+    assert time.perf_counter() - t0 < 1.0
+    assert pkg.check_status(c.ws) == bind.DEVICE_WAIT_TIMEOUT
+    out, lse = c.run()
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    c.check(out, lse)

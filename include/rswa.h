@@ -129,14 +129,18 @@ RSWA_API rswa_status rswa_check_status(void* workspace, size_t ws_bytes, int32_t
  * in flight land (bounded by the same limit) and ends the CTA, so the call returns and
  * the CUDA context stays usable. This call arms, for the NEXT decode-family call made
  * by the calling host thread only (rswa_decode*, srswa_decode*, srswa_prefill,
- * rswa_decode_noalloc; of rswa_decode_shared, its private part; consumed by that call even
- * if it fails validation):
+ * rswa_decode_noalloc, rswa_prefill_scored; consumed by that call even if it fails
+ * validation):
  *   drop_tile     : >= 0: CTA 0 neither arms nor fills the shared-memory stage of its
  *                   CTA-local tile number drop_tile, so that tile's bounded wait runs
- *                   out (no copy is in flight for it); -1: nothing dropped.
+ *                   out (no copy is in flight for it); -1: nothing dropped. Of
+ *                   rswa_decode_shared a tile of the private part, or, with
+ *                   RSWA_TEST_SHARED_PART added, a key tile of the shared part; of
+ *                   rswa_prefill_scored a key tile (of each of its launches).
  *   wait_limit_ns : the wait limit for that call, in [1e3, 1e10] ns.
  * Returns RSWA_ERR_INVALID for values out of range. Not for production use.
  */
+#define RSWA_TEST_SHARED_PART 0x40000000
 RSWA_API rswa_status rswa_test_arm_wait_timeout(int32_t drop_tile, int64_t wait_limit_ns);
 
 /*

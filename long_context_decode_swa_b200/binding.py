@@ -39,6 +39,7 @@ DEVICE_PIPELINE = 0x10
 DEVICE_BAD_RANGE = 0x20
 DEVICE_BAD_POS = 0x40
 DEVICE_BAD_SHARE = 0x80
+TEST_SHARED_PART = 0x40000000
 
 EXPORTED = ("rswa_last_error", "rswa_version", "rswa_workspace_bytes", "rswa_check_status", "rswa_append",
             "rswa_decode", "srswa_index_pool", "srswa_route", "srswa_decode", "rswa_decode_noalloc", "rswa_prefill",

@@ -1113,16 +1113,22 @@ rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_freq, const 
   return ok();
 }
 
+// A wait-timeout test's knobs: they apply to one call, whether or not it launches.
+struct TestKnobs {
+  int drop_tile = g_test_drop_tile;
+  uint64_t wait_ns = g_test_wait_ns > 0 ? g_test_wait_ns : rswa::kWaitLimitNs;
+  TestKnobs() {
+    g_test_drop_tile = -1;
+    g_test_wait_ns = 0;
+  }
+};
+
 // What the evenly cut decode calls have in common: their checks, and the arguments of the launch.
 static rswa_status balanced_args(const char* fn, const rswa_dims* dims, const void* q, const void* pk, const void* pv,
                                  const int32_t* prefix_len, const void* ring_k, const void* ring_v, const int32_t* wp,
                                  const int32_t* fill, float scale, void* out, float* lse, void* workspace,
                                  rswa::BalancedArgs* a) {
-  // a wait-timeout test knob applies to this call only, whether or not it launches
-  const int test_drop_tile = g_test_drop_tile;
-  const uint64_t test_wait_ns = g_test_wait_ns;
-  g_test_drop_tile = -1;
-  g_test_wait_ns = 0;
+  const TestKnobs test;
   rswa_status st = check_dims(fn, dims, true);
   if (st != RSWA_OK) return st;
   REQUIRE_PTR(q);
@@ -1157,8 +1163,8 @@ static rswa_status balanced_args(const char* fn, const rswa_dims* dims, const vo
   a->out = out;
   a->lse = lse;
   a->status = ws_status(workspace);
-  a->wait_limit_ns = test_wait_ns > 0 ? test_wait_ns : rswa::kWaitLimitNs;
-  a->drop_tile = test_drop_tile;
+  a->wait_limit_ns = test.wait_ns;
+  a->drop_tile = test.drop_tile;
   return RSWA_OK;
 }
 
@@ -1206,6 +1212,7 @@ rswa_status rswa_prefill_scored(const rswa_dims* dims, const rswa_score* score, 
                                 size_t ws_bytes, void* stream) {
   const char* fn = "rswa_prefill_scored";
   const NvtxRange nvtx_range(fn);
+  const TestKnobs test;
   rswa_status st = check_dims(fn, dims, true);
   if (st != RSWA_OK) return st;
   if ((st = check_score(fn, score)) != RSWA_OK) return st;
@@ -1264,6 +1271,8 @@ rswa_status rswa_prefill_scored(const rswa_dims* dims, const rswa_score* score, 
   L.wp_w = wp;
   L.fill_w = fill;
   L.status = ws_status(workspace);
+  L.wait_limit_ns = test.wait_ns;
+  L.drop_tile = test.drop_tile;
   cudaError_t e = rswa::launch_scored_prefill(L, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
@@ -1319,6 +1328,12 @@ rswa_status rswa_decode_shared(const rswa_dims* dims, int32_t n_shared, int64_t 
   L.share_of = share_of;
   L.scale = scale;
   L.status = a.status;
+  L.wait_limit_ns = a.wait_limit_ns;
+  L.drop_tile = -1;
+  if (a.drop_tile >= RSWA_TEST_SHARED_PART) {
+    L.drop_tile = a.drop_tile - RSWA_TEST_SHARED_PART;
+    a.drop_tile = -1;
+  }
   cudaError_t e = rswa::launch_shared(L, ws + 256 + align256(rswa::balanced_scratch_bytes()), &a.shared,
                                       static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = rswa::launch_balanced(a, ws + 256, static_cast<cudaStream_t>(stream));

@@ -112,6 +112,8 @@ struct Args {
   __nv_bfloat16* out;
   float* lse;
   int32_t* status;
+  uint64_t wait_limit_ns;  // of every wait
+  int drop_tile;           // a wait-timeout test: key tile that CTA 0 leaves out (-1: none)
 };
 
 enum Kind { kPrefix = 0, kRing = 1, kBand = 2 };
@@ -164,7 +166,7 @@ __device__ __forceinline__ int2 range_of(const Args& a, int m, int b, int i, boo
   return r;
 }
 
-__device__ __forceinline__ bool wait_or_abort(Smem& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
+__device__ __forceinline__ bool wait_or_abort(Smem& sm, uint64_t* bar, uint32_t parity, const Args& a) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
@@ -172,10 +174,10 @@ __device__ __forceinline__ bool wait_or_abort(Smem& sm, uint64_t* bar, uint32_t 
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&sm.abort_flag)) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+    if (global_timer_ns() - t0 > a.wait_limit_ns) break;
   }
   sm.abort_flag = 1;
-  set_status(status, RSWA_DEVICE_WAIT_TIMEOUT);
+  set_status(a.status, RSWA_DEVICE_WAIT_TIMEOUT);
   return false;
 }
 
@@ -635,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this CTA's t-th key tile
   auto tile_of = [&](int t, int& kind, int& start) { tile_kind(c, kSplit ? t * cluster + rank : t, kind, start); };
   if (warp < kSoftmaxWarp0) {
+    int issued = 0;  // by a producer: key tiles up to here
     if (warp == 0 || warp == 2) {
       // ---------------- producers: Q and K tiles (warp 0), V tiles (warp 2) ----------------
       if (lane == 0) {
@@ -650,10 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stages = is_k ? kKStages : kVStages;
         uint64_t* full = is_k ? sm.k_full : sm.v_full;
         uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
-        int t = 0;
-        for (; t < total; ++t) {
+        for (int t = 0; t < total; issued = ++t) {
           const int s = t % stages;
-          if (t >= stages && !wait_or_abort(sm, &empty[s], ((t / stages) - 1) & 1, a.status)) break;
+          if (t >= stages && !wait_or_abort(sm, &empty[s], ((t / stages) - 1) & 1, a)) break;
           int kind, start;
           tile_of(t, kind, start);
           const CUtensorMap* map = is_k ? (kind == kPrefix ? &tm_pk : (kind == kRing ? &tm_rk : &tm_ko))
@@ -663,13 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* dst = is_k ? sm.k[s] : sm.v[s];
           if (is_k && !kSplit)  // released by the arrival below
             sm.seen_by[s] = (tile_visible(c, 0, kind, start) ? 1 : 0) | (tile_visible(c, 1, kind, start) ? 2 : 0);
+          if (is_k && t == a.drop_tile && blockIdx.x == 0) continue;  // a wait-timeout test
           mbar_arrive_expect_tx(&full[s], kTileBytes);
           tma_load_2d(dst, map, 0, row, &full[s]);
           tma_load_2d(dst + kRegionBytes, map, 64, row, &full[s]);
-        }
-        if (sm.abort_flag) {  // let the copies in flight land before shared memory is released
-          if (is_k) mbar_wait(&sm.q_full, 0);
-          for (int i = max(0, t - stages); i < t; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
         }
       }
     } else if (warp == 1) {
@@ -698,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 8; ++e) {
             const int kk = (e & 1) + (e >> 1 & 1) * 4 + (e >> 2) * 2;  // both halves' first 32 columns, then their last
             if (e == 0 || (kInParts && e == 4)) {
-              if (!wait_or_abort(sm, &sm.p_full[x][kInParts ? e / 4 : 1], phase, a.status)) return false;
+              if (!wait_or_abort(sm, &sm.p_full[x][kInParts ? e / 4 : 1], phase, a)) return false;
               tc_fence_after();
             }
             tc_mma_ts(tmem + kColO + (uint32_t)x * 128u, tmem + (uint32_t)x * 128u + (uint32_t)((kk >> 2) * kHalf + (kk & 3) * 8),
@@ -707,13 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(&sm.o_done[x]);
           return true;
         };
-        bool ok = wait_or_abort(sm, &sm.q_full, 0, a.status);
+        bool ok = wait_or_abort(sm, &sm.q_full, 0, a);
         uint32_t p_phase[kQTiles] = {0, 0};
         bool more[kQTiles] = {false, false};
         int ks = 0, vs = 0;
         uint32_t k_phase = 0, v_phase = 0;
         auto take_k = [&](int& seen) {  // the next key tile has landed
-          if (!wait_or_abort(sm, &sm.k_full[ks], k_phase, a.status)) return false;
+          if (!wait_or_abort(sm, &sm.k_full[ks], k_phase, a)) return false;
           tc_fence_after();
           if (!kSplit) seen = *reinterpret_cast<volatile int*>(&sm.seen_by[ks]);
           return true;
@@ -760,12 +759,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const int t = at[x];
-            if (!(ok = wait_or_abort(sm, &sm.v_ready[x], (t >> 1) & 1, a.status))) break;
+            if (!(ok = wait_or_abort(sm, &sm.v_ready[x], (t >> 1) & 1, a))) break;
             if (!(ok = issue_pv(x, x, (t >> 1) & 1, t > 1))) break;
             tc_commit(&sm.v_empty[x]);
             if (t + 2 < total) {
               const int k = (t + 2) % kKStages;
-              if (!(ok = wait_or_abort(sm, &sm.k_full[k], ((t + 2) / kKStages) & 1, a.status))) break;
+              if (!(ok = wait_or_abort(sm, &sm.k_full[k], ((t + 2) / kKStages) & 1, a))) break;
               tc_fence_after();
               issue_s(x, k);
               tc_commit(&sm.k_empty[k]);
@@ -774,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         for (int t = 0; !kSplit && ok && t < total; ++t) {
-          if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a.status))) break;
+          if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a))) break;
           const bool next = t + 1 < total;
 #pragma unroll
           for (int x = 0; x < kQTiles; ++x) {
@@ -809,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kind == kPrefix)
           for (int r = 0; r < c.runs; ++r)
             whole |= start >= c.lo[r] && start + kRows <= c.hi[r] && (c.exact || r < kRuns - 1);
-        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[vs], (t / kVStages) & 1, a.status));
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[vs], (t / kVStages) & 1, a));
         if (!ok) break;
         if (!whole) {
           for (int r = lane; r < kRows; r += 32) {
@@ -850,6 +849,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (a.late) griddep_wait();
+    // After a give-up, which may have come long after the last copy was issued: the copies in flight land
+    // (bounded) before the CTA's shared memory goes away.
+    if ((warp == 0 || warp == 2) && lane == 0 && sm.abort_flag) {
+      const int stages = warp == 0 ? kKStages : kVStages;
+      uint64_t* full = warp == 0 ? sm.k_full : sm.v_full;
+      if (warp == 0) mbar_wait(&sm.q_full, 0, a.wait_limit_ns);
+      for (int i = max(0, issued - stages); i < issued; ++i)
+        if (warp == 2 || i != a.drop_tile || blockIdx.x != 0) mbar_wait(&full[i % stages], (i / stages) & 1, a.wait_limit_ns);
+    }
     if (warp == 1) {
       tc_fence_after();
       if (lane == 0) mbar_wait(&sm.drain, 0);  // bounded; the MMAs drain before their TMEM is freed
@@ -899,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kind, start;
       tile_of(t, kind, start);
       if (!kSplit && !tile_visible(c, x, kind, start)) continue;
-      ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], j & 1, a.status));
+      ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], j & 1, a));
       tc_fence_after();
       const RowTile rt = row_tile(c, kind, start, i, range, pos, ref);
       // does any row of this warp see one of its columns; do all rows see all of them
@@ -1045,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       given(1);
       ++j;
     }
-    if (ok && j > 0) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (j - 1) & 1, a.status));
+    if (ok && j > 0) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (j - 1) & 1, a));
     const float lse_ref = kBias ? slope2 * (float)ref : 0.f;
     sm.half[x][half][r] = l;
     if (!kSplit) {
@@ -1230,6 +1238,8 @@ cudaError_t launch_scored_prefill(const ScoredPrefillLaunch& L, cudaStream_t str
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;
   a.status = L.status;
+  a.wait_limit_ns = L.wait_limit_ns;
+  a.drop_tile = L.drop_tile;
   // Paired CTAs (each an SM, a key tile fetched once for 256 queries) in whole waves of the SMs; what is
   // left, split into 128-row tiles, in clusters as large as the SMs and the key tiles allow. A rest
   // whose tiles would not fit one wave goes paired too: two waves of half the length each.

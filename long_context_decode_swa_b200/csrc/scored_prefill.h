@@ -32,6 +32,8 @@ struct ScoredPrefillLaunch {
   int32_t* wp_w;
   int32_t* fill_w;
   int32_t* status;
+  uint64_t wait_limit_ns;  // as in BalancedArgs; the tile: the key tile of the first CTA
+  int drop_tile;
 };
 cudaError_t launch_scored_prefill(const ScoredPrefillLaunch& L, cudaStream_t stream);
 

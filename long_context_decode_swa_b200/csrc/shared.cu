@@ -243,6 +243,8 @@ struct AttnArgs {
   float scale_log2;
   SharedTables t;
   int32_t* status;
+  uint64_t wait_limit_ns;  // of every wait
+  int drop_tile;           // a wait-timeout test: key tile that CTA 0 leaves out (-1: none)
   int group;     // 1: the tables are laid out in this launch, by group_small
   GroupArgs g;
 };
@@ -329,7 +331,7 @@ __device__ void group_small(const GroupArgs& a, int* scratch) {
   __syncthreads();
 }
 
-__device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
+__device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uint32_t parity, const AttnArgs& a) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
@@ -337,10 +339,10 @@ __device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uin
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&sm.abort_flag)) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+    if (global_timer_ns() - t0 > a.wait_limit_ns) break;
   }
   sm.abort_flag = 1;
-  set_status(status, RSWA_DEVICE_WAIT_TIMEOUT);
+  set_status(a.status, RSWA_DEVICE_WAIT_TIMEOUT);
   return false;
 }
 
@@ -451,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   Walk w;
   bool more = w.begin(a.t);
+  int issued = 0;  // by a producer: key tiles up to here
   if (warp == 0 || warp == 2) {
     // ---------------- producers: K tiles (warp 0), V tiles (warp 2) ----------------
     if (lane == 0) {
@@ -459,24 +462,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t* full = is_k ? sm.k_full : sm.v_full;
       uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
       const CUtensorMap* map = is_k ? &tm_k : &tm_v;
-      int n = 0;  // tiles issued
       bool ok = true;
       for (; ok && more; more = w.next(a.t, a.H)) {
         const int row0 = (int)(((int64_t)w.t.prefix * a.H + w.h) * a.cap);
-        for (int k = w.k0; k < w.k1; ++k, ++n) {
-          const int s = n % stages;
-          if (n >= stages && !wait_or_abort(sm, &empty[s], ((n / stages) - 1) & 1, a.status)) {
+        for (int k = w.k0; k < w.k1; ++k, ++issued) {
+          const int n = issued, s = n % stages;
+          if (n >= stages && !wait_or_abort(sm, &empty[s], ((n / stages) - 1) & 1, a)) {
             ok = false;
             break;
           }
+          if (is_k && n == a.drop_tile && blockIdx.x == 0) continue;  // a wait-timeout test
           uint8_t* dst = is_k ? sm.k[s] : sm.v[s];
           mbar_arrive_expect_tx(&full[s], kTileBytes);
           tma_load_2d(dst, map, 0, row0 + k * kRows, &full[s]);
           tma_load_2d(dst + kRegionBytes, map, 64, row0 + k * kRows, &full[s]);
         }
       }
-      if (sm.abort_flag)  // let the copies in flight land before shared memory is released
-        for (int i = max(0, n - stages); i < n; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer: one thread ----------------
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(&sm.o_done[x]);
       };
       auto take_k = [&]() {
-        if (!wait_or_abort(sm, &sm.k_full[ks], k_phase, a.status)) return false;
+        if (!wait_or_abort(sm, &sm.k_full[ks], k_phase, a)) return false;
         tc_fence_after();
         return true;
       };
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto take_p = [&](int x) {
-        if (!wait_or_abort(sm, &sm.p_full[x], p_phase[x], a.status)) return false;
+        if (!wait_or_abort(sm, &sm.p_full[x], p_phase[x], a)) return false;
         p_phase[x] ^= 1;
         tc_fence_after();
         return true;
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (; ok && more; more = w.next(a.t, a.H)) {
         const int n = w.k1 - w.k0;
-        if (!(ok = wait_or_abort(sm, &sm.q_full, q_phase, a.status))) break;
+        if (!(ok = wait_or_abort(sm, &sm.q_full, q_phase, a))) break;
         q_phase ^= 1;
         tc_fence_after();
         if (w.two()) {
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         for (int t = 0; ok && t < n; ++t) {
-          if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a.status))) break;
+          if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a))) break;
           if (w.two()) {
             const bool next = t + 1 < n;
             if (!(ok = take_p(0))) break;
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && more; more = w.next(a.t, a.H)) {
       for (int k = w.k0; ok && k < w.k1; ++k, ++n) {
         const int s = n % kVStages;
-        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[s], (n / kVStages) & 1, a.status));
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[s], (n / kVStages) & 1, a));
         if (!ok) break;
         const int left = w.t.len - k * kRows;  // rows of the prefix in this tile
         if (left < kRows) {
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int events = w.events();
       for (int e = x; e < events; e += 2) {
         const int t = two ? e >> 1 : e;
-        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], seen & 1, a.status));
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], seen & 1, a));
         if (!ok) break;
         tc_fence_after();
         ++seen;
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the segment's records ----
       const bool any = x < events;
-      if (ok && any) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (seen - 1) & 1, a.status));
+      if (ok && any) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (seen - 1) & 1, a));
       // Group B without a score of its own writes nothing: it has waited for nothing in this segment, and group A
       // may still be reading the statistics of the segment before. (A group with a score has waited for scores,
       // which were issued when all threads of both groups had brought this segment's queries, past their reads.)
@@ -795,6 +796,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // After a give-up, which may have come long after the last copy was issued: the copies in flight land
+  // (bounded) before the CTA's shared memory goes away.
+  if ((warp == 0 || warp == 2) && lane == 0 && sm.abort_flag) {
+    const int stages = warp == 0 ? kKStages : kVStages;
+    uint64_t* full = warp == 0 ? sm.k_full : sm.v_full;
+    for (int i = max(0, issued - stages); i < issued; ++i)
+      if (warp == 2 || i != a.drop_tile || blockIdx.x != 0) mbar_wait(&full[i % stages], (i / stages) & 1, a.wait_limit_ns);
+  }
   if (warp == 1) {
     if (lane == 0) mbar_wait(&sm.drain, 0);  // bounded; the MMAs drain before their TMEM is freed
     __syncwarp();
@@ -869,6 +878,8 @@ cudaError_t launch_shared(const SharedLaunch& L, void* scratch, SharedTables* ta
   a.scale_log2 = L.scale * 1.4426950408889634f;
   a.t = *tables;
   a.status = L.status;
+  a.wait_limit_ns = L.wait_limit_ns;
+  a.drop_tile = L.drop_tile;
   a.group = small;
   a.g = g;
   CUtensorMap tk, tv;

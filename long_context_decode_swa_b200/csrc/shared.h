@@ -27,6 +27,8 @@ struct SharedLaunch {
   const int32_t* share_of;
   float scale;
   int32_t* status;
+  uint64_t wait_limit_ns;  // as in BalancedArgs; the tile: the key tile of the first CTA
+  int drop_tile;
 };
 // Groups the sequences and attends to the shared prefixes; *tables is for launch_balanced.
 cudaError_t launch_shared(const SharedLaunch& L, void* scratch, SharedTables* tables, cudaStream_t stream);

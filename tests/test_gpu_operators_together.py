@@ -253,3 +253,64 @@ class TestPast32Bits:
         near, _ = pkg.rswa_rope_1d(view.contiguous(), pos, freq)
         pkg.rswa_rope_1d(view, pos, freq)
         assert torch.equal(view, near)
+
+
+def _gives_up_and_recovers(run, ws, drop):
+    """run(): the outputs of a call on workspace ws. One dropped tile, then the call as before."""
+    ref = [t.clone() for t in run()]
+    assert pkg.check_status(ws) == 0
+    pkg.test_arm_wait_timeout(drop, 20_000_000)
+    t0 = time.perf_counter()
+    run()
+    torch.cuda.synchronize()
+    assert time.perf_counter() - t0 < 2.0
+    assert pkg.check_status(ws) == bind.DEVICE_WAIT_TIMEOUT
+    assert int(ws.count_nonzero()) == 0
+    for got, want in zip(run(), ref):
+        assert torch.equal(got, want)
+    assert pkg.check_status(ws) == 0
+
+
+@pytest.mark.parametrize("B,P,H,m,drop", [
+    (6, 2, 4, 300, 0),       # 24 key tiles over 24 CTAs
+    (40, 16, 12, 300, 1),    # four tiles a CTA in two segments: the second of the first segment,
+    (40, 16, 12, 300, 3),    # the last of all: every copy has been issued when its wait runs out
+    (200, 1, 5, 9000, 2),    # both query tiles: 355 key tiles, three a CTA
+    (420, 2, 2, 5000, 0),    # the same, grouped by a launch of its own
+])
+def test_shared_part_wait_timeout(cuda_lib, B, P, H, m, drop):
+    g = P64.gen(84)
+    q, sk, sv = randn((B, H, D), g), randn((P, H, m, D), g), randn((P, H, m, D), g)
+    rk, rv, wp, fill = P64.ring(B, H, 16, [16] * B, g)
+    ws = pkg.new_shared_workspace(pkg.Dims(B, H, D, 16, 0), P)
+    slen, share = ints([m] * P), ints([b % P for b in range(B)])
+
+    def run():
+        out, lse = torch.empty((B, H, D), dtype=torch.bfloat16, device="cuda"), torch.empty((B, H), device="cuda")
+        pkg.rswa_decode_shared(q, sk, sv, slen, share, rk, rv, wp, fill, out, ws, lse=lse)
+        return out, lse
+
+    _gives_up_and_recovers(run, ws, bind.TEST_SHARED_PART + drop)
+
+
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), (50.0, True)])
+@pytest.mark.parametrize("B,H,T,cap,drop", [
+    (1, 1, 100, 300, 0), (1, 1, 100, 300, 1),   # two key tiles a CTA, one a stream
+    (1, 3, 130, 2000, 0),                       # over a cluster of eight: two or three key tiles a CTA
+    (1, 3, 130, 2000, 1),
+    (2, 80, 300, 400, 0), (2, 80, 300, 400, 2),  # paired query tiles and, started early, a split rest
+    (2, 80, 300, 400, 5),                       # the last key tile: every copy has been issued when its wait runs out
+])
+def test_prefill_wait_timeout(cuda_lib, B, H, T, cap, drop, softcap, bias):
+    g = P64.gen(85)
+    q, ko, vo = (randn((B, H, T, D), g) for _ in range(3))
+    pk, pv = randn((B, H, cap, D), g), randn((B, H, cap, D), g)
+    ws, plen = torch.zeros(256, dtype=torch.uint8, device="cuda"), ints([cap] * B)
+    score = dict(slopes=torch.full((H,), 0.02, device="cuda"), pos=plen) if bias else {}
+
+    def run():
+        out, lse = torch.empty((B, H, T, D), dtype=torch.bfloat16, device="cuda"), torch.empty((B, H, T), device="cuda")
+        pkg.rswa_prefill_scored(q, ko, vo, pk, pv, plen, out, ws, softcap=softcap, lse=lse, ring=128, **score)
+        return out, lse
+
+    _gives_up_and_recovers(run, ws, drop)

@@ -13,6 +13,7 @@ import functools
 import math
 import os
 import threading
+import warnings
 
 import torch
 
@@ -99,10 +100,10 @@ def load(path: str | None = None):
         if path is None and p == _DEFAULT_LIB:
             from . import build as _build
             try:
-                if not (_build.up_to_date() and _build.ext_up_to_date()):
-                    _build.build()
+                if not _build.up_to_date():
+                    _build.build_lib()
             except RuntimeError:
-                if not os.path.exists(p) or not os.path.exists(_build.EXT):
+                if not os.path.exists(p):
                     raise
         if not os.path.exists(p):
             raise RuntimeError(f"librswa.so not found at {p}; run python -m long_context_decode_swa_b200.build")
@@ -195,13 +196,19 @@ _native = None
 
 
 def _tensors():
-    """The native tensor checks (csrc/tensors.cpp): addresses(index, spec, ..) gives the data pointers of the
-    specs' tensors, each (tensor, name, dtype, shape): contiguous, of that dtype and shape, on CUDA device
-    `index`; a fifth element lets a tensor be None. strided() gives (pointer, strides) of any layout."""
+    """The tensor checks of the newer calls: addresses(index, spec, ..) gives the data pointers of the specs'
+    tensors, each (tensor, name, dtype, shape): contiguous, of that dtype and shape, on CUDA device `index`; a
+    fifth element lets a tensor be None. strided() gives (pointer, strides) of any layout. Native
+    (csrc/tensors.cpp, built here if it is missing), or in Python (tensors.py) where it cannot be built."""
     global _native
     if _native is None:
-        load()  # builds what is missing
-        from . import _tensors as native
+        from . import build as _build
+        try:
+            _build.build_ext()
+            from . import _tensors as native
+        except (RuntimeError, ImportError) as e:
+            from . import tensors as native
+            warnings.warn(f"the tensor checks run in Python, 5 to 7 us a call more: {e}", RuntimeWarning, stacklevel=3)
         _native = native
     return _native
 

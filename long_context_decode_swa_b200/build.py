@@ -9,6 +9,7 @@ source or header is newer than the library.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -71,6 +72,8 @@ def build_ext(force: bool = False) -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[f"-I{d}" for d in includes], EXT_SRC, "-o", tmp, f"-L{os.path.join(home, 'lib')}", "-ltorch_python",
            "-ltorch_cpu", "-lc10"]
+    if shutil.which(cmd[0]) is None:
+        raise RuntimeError(f"g++ not found: it builds {EXT_SRC}")
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
@@ -78,8 +81,8 @@ def build_ext(force: bool = False) -> str:
     return EXT
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    build_ext(force)
+def build_lib(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
+    """librswa.so, which needs neither PyTorch nor Python's headers."""
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
@@ -107,6 +110,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     return LIB
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
+    """The library, then the tensor checks (left out, with a note, where there is no PyTorch or no g++)."""
+    lib = build_lib(force, verbose, extra_flags)
+    if importlib.util.find_spec("torch") is None or shutil.which("g++") is None:
+        print(f"{EXT} not built: it needs PyTorch and g++", file=sys.stderr)
+    else:
+        build_ext(force)
+    return lib
 
 
 if __name__ == "__main__":

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 import threading
@@ -195,6 +196,14 @@ def _want(t: torch.Tensor, name: str, dtype, shape=None):
 _native = None
 
 
+def _extension(path: str):
+    """The extension module `_tensors` in the file `path`."""
+    spec = importlib.util.spec_from_file_location(f"{__package__}._tensors", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
 def _tensors():
     """The tensor checks of the newer calls: addresses(index, spec, ..) gives the data pointers of the specs'
     tensors, each (tensor, name, dtype, shape): contiguous, of that dtype and shape, on CUDA device `index`; a
@@ -204,9 +213,8 @@ def _tensors():
     if _native is None:
         from . import build as _build
         try:
-            _build.build_ext()
-            from . import _tensors as native
-        except (RuntimeError, ImportError) as e:
+            native = _extension(_build.build_ext())
+        except (RuntimeError, ImportError, OSError) as e:
             from . import tensors as native
             warnings.warn(f"the tensor checks run in Python, 5 to 7 us a call more: {e}", RuntimeWarning, stacklevel=3)
         _native = native

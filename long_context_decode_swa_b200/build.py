@@ -1,5 +1,5 @@
 """Builds librswa.so in-tree from csrc/*.cu for sm_100a with nvcc, and the binding's tensor
-checks (_tensors.so, from csrc/tensors.cpp) with g++.
+checks (_tensors.<key>.so, from csrc/tensors.cpp) with g++.
 
 Run as ``python -m long_context_decode_swa_b200.build`` or call ``build()``.
 Objects go to ``long_context_decode_swa_b200/_build/`` and the library to
@@ -23,7 +23,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librswa.so")
 EXT_SRC = os.path.join(CSRC, "tensors.cpp")
-EXT = os.path.join(PKG, "_tensors.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -53,14 +52,24 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
-def ext_up_to_date() -> bool:
-    return os.path.exists(EXT) and os.path.getmtime(EXT_SRC) <= os.path.getmtime(EXT)
+def ext_path() -> str:
+    """Where the extension for this PyTorch, this Python and this source is: its name says all three, so that one
+    built against others, whose object layouts may differ, is never loaded."""
+    import hashlib
+    import sysconfig
+
+    import torch
+    with open(EXT_SRC, "rb") as f:
+        key = hashlib.sha256(f.read())
+    key.update(f"{torch.__version__} {torch.compiled_with_cxx11_abi()} {sysconfig.get_config_var('EXT_SUFFIX')}".encode())
+    return os.path.join(PKG, f"_tensors.{key.hexdigest()[:16]}.so")
 
 
 def build_ext(force: bool = False) -> str:
     """The CPython extension that checks tensors (no CUDA in it)."""
-    if not force and ext_up_to_date():
-        return EXT
+    ext = ext_path()
+    if not force and os.path.exists(ext):
+        return ext
     import sysconfig
 
     import torch
@@ -68,7 +77,7 @@ def build_ext(force: bool = False) -> str:
     home = os.path.dirname(torch.__file__)
     includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"]]
-    tmp = EXT + f".tmp{os.getpid()}"
+    tmp = ext + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[f"-I{d}" for d in includes], EXT_SRC, "-o", tmp, f"-L{os.path.join(home, 'lib')}", "-ltorch_python",
            "-ltorch_cpu", "-lc10"]
@@ -77,8 +86,8 @@ def build_ext(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, EXT)
-    return EXT
+    os.replace(tmp, ext)
+    return ext
 
 
 def build_lib(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -116,7 +125,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     """The library, then the tensor checks (left out, with a note, where there is no PyTorch or no g++)."""
     lib = build_lib(force, verbose, extra_flags)
     if importlib.util.find_spec("torch") is None or shutil.which("g++") is None:
-        print(f"{EXT} not built: it needs PyTorch and g++", file=sys.stderr)
+        print(f"{EXT_SRC} not built: it needs PyTorch and g++", file=sys.stderr)
     else:
         build_ext(force)
     return lib

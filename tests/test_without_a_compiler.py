@@ -89,3 +89,25 @@ def test_python_and_native_checks_agree(cuda_lib):
         for checks in (tensors, native):
             with pytest.raises(ValueError):
                 checks.addresses(index, spec)
+
+
+def test_the_extension_is_of_this_pytorch_python_and_source(monkeypatch, tmp_path):
+    import sysconfig
+    here = build.ext_path()
+    assert build.ext_path() == here and os.path.dirname(here) == build.PKG
+    seen = {here}
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", torch.__version__ + ".later")
+        seen.add(build.ext_path())
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-x86_64-linux-gnu.so")
+        seen.add(build.ext_path())
+    with monkeypatch.context() as m:
+        m.setattr(torch, "compiled_with_cxx11_abi", lambda: not torch._C._GLIBCXX_USE_CXX11_ABI)
+        seen.add(build.ext_path())
+    other = tmp_path / "tensors.cpp"
+    with open(build.EXT_SRC) as f:
+        other.write_text(f.read() + "\n// changed\n")
+    monkeypatch.setattr(build, "EXT_SRC", str(other))
+    seen.add(build.ext_path())
+    assert len(seen) == 5

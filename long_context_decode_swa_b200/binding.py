@@ -207,7 +207,8 @@ def _extension(path: str):
 def _tensors():
     """The tensor checks of the newer calls: addresses(index, spec, ..) gives the data pointers of the specs'
     tensors, each (tensor, name, dtype, shape): contiguous, of that dtype and shape, on CUDA device `index`; a
-    fifth element lets a tensor be None. strided() gives (pointer, strides) of any layout. Native
+    fifth element lets a tensor be None. strided() gives (pointer, strides) of any layout, and refuses tensors
+    that require a gradient while autograd records one. Native
     (csrc/tensors.cpp, built here if it is missing), or in Python (tensors.py) where it cannot be built."""
     global _native
     if _native is None:
@@ -367,7 +368,9 @@ def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str =
     tensor may be a strided view with a dense last axis. inv_freq: f64 pair frequencies on the host
     (a CPU tensor; see rope_freqs); its length is half the rotated dims, the rest of a head passes
     through. layout: "half" or "interleaved" pairs. inverse=True applies the transpose, which turns
-    gradients back. Outputs default to in place. Returns (q_out, k_out)."""
+    gradients back. Outputs default to in place. Returns (q_out, k_out). The call records nothing for autograd and
+    refuses tensors that require a gradient while one is recorded: call it from an autograd.Function (forward, and
+    with inverse=True backward) or under torch.no_grad()."""
     dev = _device_of(q, "q")
     shape, dtype = tuple(q.shape), q.dtype
     if len(shape) not in (3, 4):

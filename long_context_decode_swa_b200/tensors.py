@@ -28,6 +28,9 @@ def _checked(index: int, spec, dense: bool):
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
     if dense and not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
+    if not dense and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires a gradient, and the call records none (call it from an autograd.Function "
+                         "or under torch.no_grad())")
     return t
 
 
@@ -39,7 +42,8 @@ def addresses(index, *specs):
 
 
 def strided(index, *specs):
-    """(data pointer, strides) of tensors that need not be contiguous."""
+    """(data pointer, strides) of tensors that need not be contiguous; none may require a gradient that autograd
+    would record."""
     index = operator.index(index)
     found = [_checked(index, s, False) for s in specs]
     return tuple(None if t is None else (t.data_ptr(), t.stride()) for t in found)

@@ -205,3 +205,36 @@ def test_refusals_on_device_tensors(cuda_lib):
                 lambda: call(q, pos, freq, q_out=torch.empty_like(q)[:, :1].expand(2, 4, 6, 128))):
         with pytest.raises(cuda_lib.RswaError):
             bad()
+
+
+def test_tensors_that_require_a_gradient(cuda_lib):
+    # refused while autograd records, whichever tensor it is; taken where it does not; and the gradient of an
+    # autograd.Function of the call and its transpose against the formula's
+    freq, _ = pkg.rope_freqs(64)
+    q, k = rows((1, 2, 9, 96), 51, torch.float32), rows((1, 1, 9, 96), 52, torch.float32)
+    pos, out = positions(1, 9, 53, 0, 9000), torch.empty_like(q)
+    leaf, leaf_k = q.clone().requires_grad_(), k.clone().requires_grad_()
+    for bad in (lambda: cuda_lib.rswa_rope_1d(leaf, pos, freq, q_out=out), lambda: cuda_lib.rswa_rope_1d(leaf, pos, freq),
+                lambda: cuda_lib.rswa_rope_1d(leaf * 2, pos, freq, q_out=out),
+                lambda: cuda_lib.rswa_rope_1d(q, pos, freq, q_out=leaf),
+                lambda: cuda_lib.rswa_rope_1d(q, pos, freq, q_out=out, k=leaf_k, k_out=torch.empty_like(k)),
+                lambda: cuda_lib.rswa_rope_1d(q, pos, freq, q_out=out, k=k, k_out=leaf_k)):
+        with pytest.raises(ValueError, match="gradient"):
+            bad()
+    assert torch.equal(leaf, q) and torch.equal(leaf_k, k)
+    with torch.no_grad():
+        cuda_lib.rswa_rope_1d(leaf, pos, freq, q_out=out)
+    check(out, q, pos, freq, "half")
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return cuda_lib.rswa_rope_1d(x, pos, freq, q_out=torch.empty_like(x))[0]
+
+        @staticmethod
+        def backward(ctx, g):
+            return cuda_lib.rswa_rope_1d(g.contiguous(), pos, freq, q_out=torch.empty_like(g), inverse=True)[0]
+
+    g = rows(q.shape, 54, torch.float32)
+    (Rope.apply(leaf) * g).sum().backward()
+    check(leaf.grad, g, pos, freq, "half", inverse=True)

@@ -85,6 +85,12 @@ def test_python_and_native_checks_agree(cuda_lib):
     good = [(t, "t", BF16, (4, 3, 8)), (t[1], "u", BF16, (3, 8)), (None, "n", BF16, (1,), True)]
     assert tensors.addresses(i, *good) == native.addresses(i, *good)
     assert tensors.strided(i, (v, "v", BF16, (3, 4, 8))) == native.strided(i, (v, "v", BF16, (3, 4, 8)))
+    leaf = t.float().requires_grad_()
+    for checks in (tensors, native):
+        with pytest.raises(ValueError, match="gradient"):
+            checks.strided(i, (leaf, "leaf", torch.float32, (4, 3, 8)))
+        with torch.no_grad():
+            checks.strided(i, (leaf, "leaf", torch.float32, (4, 3, 8)))
     for index, spec in [(i, (v, "v", BF16, (3, 4, 8))), (i, (t, "t", BF16, (4, 3))), (i + 1, good[0])]:
         for checks in (tensors, native):
             with pytest.raises(ValueError):

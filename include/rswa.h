@@ -571,8 +571,8 @@ RSWA_API rswa_status srswa_step_rope(const rswa_dims* dims, const rswa_rope* rop
  *     dtype    : RSWA_DTYPE_BF16 or RSWA_DTYPE_F32, of every tensor
  *     mscale   : finite factor on cos and sin (1 unless the scaling has one)
  *     *_stride : strides of the batch, head and token axes in elements, each a multiple of 16
- *                bytes (any order of the axes; the last axis is dense). Output rows must not
- *                overlap one another.
+ *                bytes (any order of the axes; the last axis is dense; not looked at for an axis
+ *                of one entry). Output rows must not overlap one another.
  *   inv_freq : HOST array f64 [rot_dim / 2], finite, read during the call only
  *   pos      : int32 [batch][tokens], any values
  *   q_out / k_out may be q / k with the same strides (in place; dims from rot_dim on then keep

@@ -361,6 +361,11 @@ def _rope_desc(dtype, layout, mscale, inverse, pairs, shape, heads_k, *strides):
     return d
 
 
+def _same_rows(shape, a, b) -> bool:
+    """Whether strides a and b lay the rows of `shape` out alike (an axis of one entry has no say)."""
+    return 0 in shape or all(n == 1 or x == y for n, x, y in zip(shape, a, b))
+
+
 def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str = "half", mscale: float = 1.0,
                  inverse: bool = False, stream=None):
     """Rotary encoding of q (and k), bf16 or f32 [B][H][T][D] at int32 positions pos [B][T], or [B][H][D]
@@ -399,10 +404,10 @@ def rswa_rope_1d(q, pos, inv_freq, q_out=None, k=None, k_out=None, layout: str =
         (qp, qs), (qop, qos), (kp, ks), (kop, kos) = native.strided(
             dev, (q, "q", dtype, shape), (q_out, "q_out", dtype, shape), (k, "k", dtype, kshape),
             (k_out, "k_out", dtype, kshape))
-        if kp == kop and ks != kos:
+        if kp == kop and ks != kos and not _same_rows(kshape, ks, kos):
             raise ValueError("k_out: in place needs the input's strides")
         d = _rope_desc(dtype, layout, mscale, inverse, inv_freq.shape[0], shape, kshape[1], qs, qos, ks, kos)
-    if qp == qop and qs != qos:
+    if qp == qop and qs != qos and not _same_rows(shape, qs, qos):
         raise ValueError("q_out: in place needs the input's strides")
     _call("rswa_rope_1d", dev, stream, d, inv_freq.data_ptr(), pos_p, qp, qop, kp, kop)
     return q_out, k_out

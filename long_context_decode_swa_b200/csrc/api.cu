@@ -1067,7 +1067,7 @@ rswa_status rswa_rope_1d(const rswa_rope1d* desc, const double* inv_freq, const 
   for (int i = 0; i < (d.heads_k > 0 ? 4 : 2); ++i) {
     const int32_t extent[3] = {d.batch, i < 2 ? d.heads_q : d.heads_k, d.tokens};
     for (int j = 0; j < 3; ++j) {
-      if (all[i][j] % vec != 0)
+      if (extent[j] > 1 && all[i][j] % vec != 0)
         return fail(RSWA_ERR_INVALID, "%s: strides of %s must be multiples of 16 bytes", fn, names[i]);
       if ((i & 1) && extent[j] > 1 && all[i][j] == 0)
         return fail(RSWA_ERR_INVALID, "%s: rows of %s overlap (a stride of 0)", fn, names[i]);

@@ -238,3 +238,25 @@ def test_tensors_that_require_a_gradient(cuda_lib):
     g = rows(q.shape, 54, torch.float32)
     (Rope.apply(leaf) * g).sum().backward()
     check(leaf.grad, g, pos, freq, "half", inverse=True)
+
+
+def test_strides_of_axes_of_one_entry_do_not_matter(cuda_lib):
+    # one sequence, one token, one head: such an axis may have any stride (views and slices give it odd ones), in
+    # place too, where input and output may differ in it; and empty tensors of any strides
+    freq, _ = pkg.rope_freqs(64)
+    for shape, odd, other in [((1, 4, 6, 128), (7, 768, 128, 1), (3, 768, 128, 1)), ((2, 4, 1, 128), (512, 128, 5, 1), (512, 128, 128, 1)),
+                              ((3, 1, 2, 128), (256, 13, 128, 1), (256, 0, 128, 1))]:
+        x = rows((3 * 1024,), 61)
+        keep = x.clone()
+        pos = positions(shape[0], shape[2], 62, 0, 5000)
+        plain = keep.as_strided(shape, (odd[0] if shape[0] > 1 else 4096, odd[1] if shape[1] > 1 else 4096,
+                                        odd[2] if shape[2] > 1 else 4096, 1)).contiguous()
+        want, _ = cuda_lib.rswa_rope_1d(plain, pos, freq, q_out=torch.empty_like(plain))
+        got, _ = cuda_lib.rswa_rope_1d(x.as_strided(shape, odd), pos, freq, q_out=torch.empty_like(plain))
+        assert torch.equal(got, want)
+        got, gk = cuda_lib.rswa_rope_1d(x.as_strided(shape, odd), pos, freq, q_out=x.as_strided(shape, other),
+                                        k=plain, k_out=plain.as_strided(shape, plain.stride()))
+        assert torch.equal(got, want) and torch.equal(gk, want)
+    empty = torch.empty((0, 4, 6, 128), dtype=torch.bfloat16, device="cuda")
+    turned = torch.empty((0, 6, 4, 128), dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    assert cuda_lib.rswa_rope_1d(empty, positions(0, 6, 63), freq, q_out=turned)[0] is turned

@@ -978,6 +978,14 @@ def srswa_step_rope(q, k_new, v_new, q_idx, kbar, pk, pv, prefix_len, ring_k, ri
         _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
+def _int32(value, name: str) -> int:
+    """An integer that fits the C argument (ctypes would cut it)."""
+    n = int(value)
+    if n != value or not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}: {value} is not an integer of 32 bits")
+    return n
+
+
 def _numel(t, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
@@ -1041,7 +1049,7 @@ def rswa_prefill_scored(q, k_out, v_out, pk, pv, prefix_len, out, workspace, sof
             raise ValueError("without a ring tensor, pass the window length as ring=n")
         if ring_v is not None or wp is not None or fill is not None:
             raise ValueError("ring_k, ring_v, wp and fill go together")
-        n, ring_shape = int(ring), ()
+        n, ring_shape = _int32(ring, "ring"), ()
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     ws_bytes = _numel(workspace, "workspace")
     ring_specs = ((ring_k, "ring_k", bf16, ring_shape), (ring_v, "ring_v", bf16, ring_shape), (wp, "wp", i32, (B,)),
@@ -1057,7 +1065,7 @@ def rswa_prefill_scored(q, k_out, v_out, pk, pv, prefix_len, out, workspace, sof
 
 def shared_workspace_bytes(dims: Dims, n_shared: int) -> int:
     """Workspace bytes of rswa_decode_shared; dims.prefix_cap is the private capacity."""
-    n = load().rswa_decode_shared_workspace_bytes(ctypes.byref(dims), n_shared)
+    n = load().rswa_decode_shared_workspace_bytes(ctypes.byref(dims), _int32(n_shared, "n_shared"))
     if n == 0:
         raise RswaError("rswa_decode_shared_workspace_bytes", 1, load().rswa_last_error().decode())
     return int(n)

@@ -362,3 +362,13 @@ def test_a_workspace_that_says_timeout_costs_no_waits(cuda_lib, B, H, T):
     out, lse = c.run()
     assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
     c.check(out, lse)
+
+
+def test_a_window_past_32_bits_is_refused(cuda_lib):
+    c = Case(1, 1, 4, 8, seed=67)
+    for n, err in ((2 ** 32 + 128, ValueError), (2 ** 31, ValueError), (1025, pkg.RswaError), (128.5, ValueError)):
+        c.n = n
+        with pytest.raises(err):
+            c.run()
+    c.n = 128.0
+    c.run()

@@ -120,3 +120,11 @@ def _prefill(**kw):
 def test_prefill_scored_refusals(kw, code, word):
     got, msg = _prefill(**kw)
     assert got == code and word in msg, (got, msg)
+
+
+def test_integers_past_32_bits_are_refused():
+    # (cut to 32 bits they would be a size of 3)
+    for n in (2 ** 32 + 3, -2 ** 32 + 3, 2 ** 31):
+        with pytest.raises(ValueError, match="n_shared"):
+            rswa.shared_workspace_bytes(DIMS, n)
+    assert rswa.shared_workspace_bytes(DIMS, 3) == rswa.load().rswa_decode_shared_workspace_bytes(ctypes.byref(DIMS), 3)

@@ -372,3 +372,108 @@ def test_a_window_past_32_bits_is_refused(cuda_lib):
             c.run()
     c.n = 128.0
     c.run()
+
+
+@pytest.mark.parametrize("largest", [0.399, 0.999, 12.0])
+def test_capped_scores_by_each_form_of_the_tanh(cuda_lib, largest):
+    # Queries that see only themselves (a window of one): lse is the score. The rows of a head are multiples of unit
+    # vectors, so that every other score is 0, and a warp takes the form that its largest |u| = |scale q.k| / cap calls
+    # for. In units of the cap: the polynomials are within 2e-8; ten f32 roundings (cap log2(e) 2, scale / cap 1, the
+    # coefficient 2, Horner's last steps and the product 3, ln 2 and its product 2) of a value of at most tanh(largest).
+    # The exponential form adds ex2's and rcp's errors (2^-22 of e^2u: 2^-23; 2^-23 of 2 / (e^2u + 1): 2^-22), the
+    # argument's three roundings (u sech^2 u <= 0.45: 0.45 * 3 * 2^-24) and the sum's (2^-24).
+    H, T, cap, scale = 96, 128, 50.0, 0.125
+    g = torch.Generator("cuda")
+    g.manual_seed(71)
+    u = (torch.rand((1, H, T), generator=g, device="cuda", dtype=torch.float64) * 2 - 1) * largest
+    a = (torch.rand((1, H, T), generator=g, device="cuda", dtype=torch.float64) + 1).bfloat16()
+    b = (u * cap / scale / a.double()).bfloat16()
+    over = (a.double() * b.double()).abs() * scale / cap > largest
+    b = torch.where(over, (b.double() * 0.99).bfloat16(), b)
+    eye = torch.eye(D, device="cuda", dtype=torch.bfloat16)[None, None]
+    q, k = eye * a[..., None], eye * b[..., None]
+    none = torch.empty((1, H, 0, D), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((1, H, T), device="cuda")
+    pkg.rswa_prefill_scored(q.contiguous(), k.contiguous(), q.contiguous(), none, none, ints([0]), out,
+                            torch.zeros(256, dtype=torch.uint8, device="cuda"), softcap=cap, scale=scale, ring=1, lse=lse)
+    u = a.double() * b.double() * scale / cap
+    err = ((lse.double() / cap) - torch.tanh(u)).abs().max().item()
+    print(f"largest |u| {largest}: error {err:.2e} of the cap")
+    bound = 2e-8 + 10 * 2.0 ** -24 * math.tanh(largest)
+    if largest > 1:
+        bound += 2.0 ** -23 + 2.0 ** -22 + 0.45 * 3 * 2.0 ** -24 + 2.0 ** -24
+    assert u.abs().max().item() > 0.97 * largest
+    assert err <= bound, (err, bound)
+
+
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), (30.0, True)])
+def test_a_nan_value_row_stays_in_its_256_queries(cuda_lib, softcap, bias):
+    # a NaN row of V that some query sees reaches at most the 256 queries of that query's tile (0 x NaN): queries of
+    # other tiles, of the same and of other documents, are what they are without it
+    T, cap = 700, 900
+    ranges = [[(0, 300) if i < 100 else (300, 900) for i in range(T)]]
+    c = Case(1, 3, T, cap, ranges=ranges, softcap=softcap, slopes=slopes_of(3) if bias else None, pos=[cap] if bias else None, seed=68)
+    ref = c.run()
+    c.pv[:, :, 77] = math.nan
+    out, lse = c.run()
+    assert out[:, :, :100].isnan().all()
+    assert torch.equal(out[:, :, 256:], ref[0][:, :, 256:]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_chunks_with_an_early_started_rest(cuda_lib, captured):
+    # Two launches a chunk, the second started early beside the first: inputs written just before them (by a copy, and
+    # by a rotary call that starts early itself), the ring moved right after them, chunk upon chunk without a pause,
+    # eagerly and from a graph, against the same calls one at a time
+    B, H, T, n, cap = 2, 80, 300, 128, 300
+    c = Case(B, H, T, cap, n=n, fill=[128, 60], softcap=30.0, slopes=slopes_of(H), pos=[cap, cap + 9],
+             ranges=[[(0, 200)] * 150 + [(100, 300)] * 150] * B, seed=69)
+    g = P64.gen(70)
+    chunks = [tuple(randn((B, H, T, D), g, s) for s in (2.0, 1.0, 1.0)) for _ in range(4)]
+    freq, _ = pkg.rope_freqs(128)
+    at = torch.arange(T, dtype=torch.int32, device="cuda").expand(B, T).contiguous()
+    state = [t.clone() for t in (c.rk, c.rv, c.wp, c.fill, c.pos, c.ranges)]
+    src = [torch.empty_like(x) for x in chunks[0]]
+    q, k = torch.empty_like(c.q), torch.empty_like(c.ko)
+    out, lse = torch.empty_like(c.q), torch.empty((B, H, T), device="cuda")
+
+    def chunk(wait=lambda: None):
+        c.vo.copy_(src[2])
+        wait()
+        pkg.rswa_rope_1d(src[0], at, freq, q_out=q, k=src[1], k_out=k)
+        wait()
+        pkg.rswa_prefill_scored(q, k, c.vo, c.pk, c.pv, c.plen, out, c.ws, softcap=30.0, slopes=c.slopes, pos=c.pos,
+                                ranges=c.ranges, lse=lse, ring_k=c.rk, ring_v=c.rv, wp=c.wp, fill=c.fill, write_ring=True)
+        wait()
+        c.pos.add_(T)
+        c.ranges.copy_(torch.roll(c.ranges, 40, 1))
+
+    def restart():
+        for t, s in zip((c.rk, c.rv, c.wp, c.fill, c.pos, c.ranges), state):
+            t.copy_(s)
+
+    refs = []
+    for x in chunks:
+        for s, t in zip(src, x):
+            s.copy_(t)
+        chunk(torch.cuda.synchronize)
+        refs.append((out.clone(), lse.clone(), c.rk.clone(), c.rv.clone(), c.wp.clone(), c.fill.clone()))
+    restart()
+    step = chunk
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chunk()
+        step = graph.replay
+    for _ in range(3):
+        got = []
+        restart()
+        for x in chunks:
+            for s, t in zip(src, x):
+                s.copy_(t)
+            step()
+            got.append((out.clone(), lse.clone(), c.rk.clone(), c.rv.clone(), c.wp.clone(), c.fill.clone()))
+        torch.cuda.synchronize()
+        for a, b in zip(got, refs):
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+    assert pkg.check_status(c.ws) == 0

@@ -105,6 +105,13 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   return p;
 }
 
+// Lets the last of a producer's copies 0 .. issued - 1, of `stages` mbarriers in turn, land (bounded); `dropped` was
+// never issued. For a CTA that ends after a give-up; not inlined, to keep it out of the kernels' instruction cache.
+static __device__ __noinline__ void land_copies(uint64_t* full, int stages, int issued, int dropped, uint64_t limit_ns) {
+  for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+    if (i != dropped) mbar_wait(&full[i % stages], (i / stages) & 1, limit_ns);
+}
+
 // bf16x2 word -> two floats (low half is the element at the lower address).
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

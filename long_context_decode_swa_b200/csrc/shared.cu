@@ -228,6 +228,7 @@ struct SharedSmem {
   uint64_t v_full[kVStages], v_ready[kVStages], v_empty[kVStages];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t drain;
+  uint64_t wait_limit_ns;  // of every wait
   uint32_t tmem_base;
   int abort_flag;
   float stat_m[2][kRows];              // at a segment's end: both groups' maxima,
@@ -243,7 +244,7 @@ struct AttnArgs {
   float scale_log2;
   SharedTables t;
   int32_t* status;
-  uint64_t wait_limit_ns;  // of every wait
+  uint64_t wait_limit_ns;
   int drop_tile;           // a wait-timeout test: key tile that CTA 0 leaves out (-1: none)
   int group;     // 1: the tables are laid out in this launch, by group_small
   GroupArgs g;
@@ -331,7 +332,7 @@ __device__ void group_small(const GroupArgs& a, int* scratch) {
   __syncthreads();
 }
 
-__device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uint32_t parity, const AttnArgs& a) {
+__device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
@@ -339,10 +340,10 @@ __device__ __forceinline__ bool wait_or_abort(SharedSmem& sm, uint64_t* bar, uin
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&sm.abort_flag)) return false;
-    if (global_timer_ns() - t0 > a.wait_limit_ns) break;
+    if (global_timer_ns() - t0 > *reinterpret_cast<volatile uint64_t*>(&sm.wait_limit_ns)) break;
   }
   sm.abort_flag = 1;
-  set_status(a.status, RSWA_DEVICE_WAIT_TIMEOUT);
+  set_status(status, RSWA_DEVICE_WAIT_TIMEOUT);
   return false;
 }
 
@@ -419,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     sm.abort_flag = 0;
+    sm.wait_limit_ns = a.wait_limit_ns;
     mbar_init(&sm.q_full, 256);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&sm.k_full[s], 1);
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row0 = (int)(((int64_t)w.t.prefix * a.H + w.h) * a.cap);
         for (int k = w.k0; k < w.k1; ++k, ++issued) {
           const int n = issued, s = n % stages;
-          if (n >= stages && !wait_or_abort(sm, &empty[s], ((n / stages) - 1) & 1, a)) {
+          if (n >= stages && !wait_or_abort(sm, &empty[s], ((n / stages) - 1) & 1, a.status)) {
             ok = false;
             break;
           }
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(&sm.o_done[x]);
       };
       auto take_k = [&]() {
-        if (!wait_or_abort(sm, &sm.k_full[ks], k_phase, a)) return false;
+        if (!wait_or_abort(sm, &sm.k_full[ks], k_phase, a.status)) return false;
         tc_fence_after();
         return true;
       };
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto take_p = [&](int x) {
-        if (!wait_or_abort(sm, &sm.p_full[x], p_phase[x], a)) return false;
+        if (!wait_or_abort(sm, &sm.p_full[x], p_phase[x], a.status)) return false;
         p_phase[x] ^= 1;
         tc_fence_after();
         return true;
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (; ok && more; more = w.next(a.t, a.H)) {
         const int n = w.k1 - w.k0;
-        if (!(ok = wait_or_abort(sm, &sm.q_full, q_phase, a))) break;
+        if (!(ok = wait_or_abort(sm, &sm.q_full, q_phase, a.status))) break;
         q_phase ^= 1;
         tc_fence_after();
         if (w.two()) {
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         for (int t = 0; ok && t < n; ++t) {
-          if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a))) break;
+          if (!(ok = wait_or_abort(sm, &sm.v_ready[vs], v_phase, a.status))) break;
           if (w.two()) {
             const bool next = t + 1 < n;
             if (!(ok = take_p(0))) break;
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && more; more = w.next(a.t, a.H)) {
       for (int k = w.k0; ok && k < w.k1; ++k, ++n) {
         const int s = n % kVStages;
-        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[s], (n / kVStages) & 1, a));
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.v_full[s], (n / kVStages) & 1, a.status));
         if (!ok) break;
         const int left = w.t.len - k * kRows;  // rows of the prefix in this tile
         if (left < kRows) {
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int events = w.events();
       for (int e = x; e < events; e += 2) {
         const int t = two ? e >> 1 : e;
-        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], seen & 1, a));
+        ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.s_full[x], seen & 1, a.status));
         if (!ok) break;
         tc_fence_after();
         ++seen;
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the segment's records ----
       const bool any = x < events;
-      if (ok && any) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (seen - 1) & 1, a));
+      if (ok && any) ok = __all_sync(0xffffffffu, wait_or_abort(sm, &sm.o_done[x], (seen - 1) & 1, a.status));
       // Group B without a score of its own writes nothing: it has waited for nothing in this segment, and group A
       // may still be reading the statistics of the segment before. (A group with a score has waited for scores,
       // which were issued when all threads of both groups had brought this segment's queries, past their reads.)
@@ -798,12 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   // After a give-up, which may have come long after the last copy was issued: the copies in flight land
   // (bounded) before the CTA's shared memory goes away.
-  if ((warp == 0 || warp == 2) && lane == 0 && sm.abort_flag) {
-    const int stages = warp == 0 ? kKStages : kVStages;
-    uint64_t* full = warp == 0 ? sm.k_full : sm.v_full;
-    for (int i = max(0, issued - stages); i < issued; ++i)
-      if (warp == 2 || i != a.drop_tile || blockIdx.x != 0) mbar_wait(&full[i % stages], (i / stages) & 1, a.wait_limit_ns);
-  }
+  if ((warp == 0 || warp == 2) && lane == 0 && sm.abort_flag)
+    land_copies(warp == 0 ? sm.k_full : sm.v_full, warp == 0 ? kKStages : kVStages, issued,
+                warp == 0 && blockIdx.x == 0 ? a.drop_tile : -1, a.wait_limit_ns);
   if (warp == 1) {
     if (lane == 0) mbar_wait(&sm.drain, 0);  // bounded; the MMAs drain before their TMEM is freed
     __syncwarp();

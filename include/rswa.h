@@ -577,8 +577,8 @@ RSWA_API rswa_status srswa_step_rope(const rswa_dims* dims, const rswa_rope* rop
  *   pos      : int32 [batch][tokens], any values
  *   q_out / k_out may be q / k with the same strides (in place; dims from rot_dim on then keep
  *   their values); other overlaps of an output with an input are not supported.
- * Arithmetic: the angle as a 64-bit fixed-point fraction of a turn (error below 2^-31 max(1, |inv_freq|) turns
- * for every int32 position), cos / sin and the rotation in f32, one rounding to bf16: within
+ * Arithmetic: the angle as a 64-bit fixed-point fraction of a turn (error below 2^-31 (1 + |inv_freq|) turns
+ * for every int32 position), then rounded to f32; cos / sin and the rotation in f32, one rounding to bf16: within
  * 2^-20 (|x| + |y|) |mscale| plus half a bf16 step of the exact rotation by the table's angles.
  */
 #define RSWA_ROPE_HALF 0
@@ -641,9 +641,13 @@ RSWA_API rswa_status rswa_decode_scored(const rswa_dims* dims, const rswa_score*
  *           document a query
  *   out   : bf16 [B][H][T][D] (P is rounded to bf16 for P V, and more bits would carry nothing);
  *           lse : f32 [B][H][T] or NULL, from unrounded weights
- * Prefix tiles of 128 rows that no query of a 256-query tile sees are skipped. Prefix rows that no
- * query of such a tile sees, and rows past a length, may hold anything; a non-finite row that
- * some query of the tile sees can reach the tile's other queries.
+ * Prefix tiles of 128 rows that no query of a 256-query tile sees are skipped, as long as the tile's
+ * ranges make up at most four separate runs of rows; further runs are taken as one, gaps and all,
+ * and every tile of that one which is not seen whole costs some 100 us more (documents that follow
+ * one another make one run). Prefix rows that no query of a 256-query tile sees, and rows past a
+ * length, may hold anything (with a cap, a score's last bits can depend on them: the tanh is taken
+ * by one of three forms, within 3e-7 of the cap, by the scores around); a non-finite row that some
+ * query of the tile sees can reach the tile's other queries.
  * prefix_cap may be 0 (pk, pv and prefix_len are then not read).
  */
 RSWA_API rswa_status rswa_prefill_scored(const rswa_dims* dims, const rswa_score* score, int32_t T, const void* q,

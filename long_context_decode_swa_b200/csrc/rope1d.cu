@@ -6,10 +6,12 @@
 // transpose, which turns gradients back, is the same with -s.
 //
 // The angle is kept as a fraction of a turn in 64-bit fixed point: the host gives
-// frac(inv_freq / 2 pi) * 2^64, the kernel multiplies by the integer position modulo 2^64
-// (whole turns fall off the top), and the 32 leading bits go to sincospif. That is exact to
-// |pos| * 2^-65 + 2^-32 turns for every int32 position without fp64 arithmetic, whose rate
+// frac(inv_freq / 2 pi) * 2^64 (its lowest bit 0), the kernel multiplies by the integer position
+// modulo 2^64 (whole turns fall off the top) and keeps the 32 leading bits: exact to
+// |pos| * 2^-63 + 2^-32 turns for every int32 position without fp64 arithmetic, whose rate
 // on this chip would bound the kernel (the page2d kernel's fp64 sincos is its second cost).
+// The 32 bits are rounded to f32 (by at most 2^-26 turns) for sincospif, of f32 rows; of bf16
+// rows they are taken times 2 pi / 2^32 (3.1e-7 in all, at most) for __sincosf.
 //
 // HBM-bound: every element is read once and written once. A warp takes the rows of a few
 // consecutive tokens (four at 128 bf16 dims: 1 KiB runs) in up to 8 heads, four heads at a time in
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope1d_kernel(const __grid_consta
         const uint64_t turn = (uint64_t)(int64_t)pos * a.turns[c * N + i];
         const float part = (float)(int32_t)(turn >> 32);  // of a turn, times 2^32: half a turn either way
         float s, co;
-        if (sizeof(E) == 2)  // good to 2^-21.2 here, far below a bf16 step
+        if (sizeof(E) == 2)  // its own error is at most 2^-21.2 up to pi, far below a bf16 step
           __sincosf(part * 1.4629180792671596e-9f, &s, &co);  // 2 pi / 2^32
         else
           sincospif(part * 4.656612873077393e-10f, &s, &co);  // 2^-31

@@ -17,7 +17,10 @@
 //
 // Documents: the union of the rows' ranges, as up to four runs of rows, gives the prefix tiles;
 // rows of a tile that no query of the CTA sees are zeroed in V (0 * NaN would reach O). A chunk over
-// packed documents so costs what its documents cost, not what the prefix does.
+// packed documents so costs what its documents cost, not what the prefix does, while a CTA's queries
+// see at most four runs. What lies past the third run is taken as one run with its gaps, whose
+// unseen rows are found query by query: 16 heads x 2304 queries, each 256 of them over eight documents of
+// 300 rows, take 65 us where the documents touch and 6,600 us with gaps of 300 rows between them.
 //
 // What bounds it: a tile's MMAs take 1,024 cycles, and one ex2 a score as many of the special-function
 // unit (16 a cycle and SM); a stream's chain of scores, maximum, exponentials and P V takes some 5,000, of which
@@ -26,7 +29,8 @@
 //
 // Scores: tanh(u) = 1 - 2 / (e^2u + 1) would cost two more special-function operations; where a warp's
 // scores all have |u| = |scale q.k| / cap <= 0.4 (or 1), tanh is u times a minimax polynomial in u^2
-// instead, on the packed FMA pipe (errors below 1e-7 of the cap either way).
+// instead, on the packed FMA pipe. Scores against 64 bits, in units of the cap, at 12,288 points each: within
+// 6.3e-8 (|u| up to 0.4), 1.4e-7 (up to 1) and 2.9e-7 (any, by the two operations).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -228,7 +232,8 @@ __device__ __forceinline__ float2 ex2_pair(float2 z) {
 // x 10272 rows take 185 us instead of 188, and x 1152 queries 102 instead of 108. (Capped ones keep the FMA pipe busy.)
 constexpr int kPolyPairs = 4;
 
-// tanh(u) = u p(u^2): minimax polynomials, within 2e-8 for |u| up to 0.4 and up to 1 (four and seven terms).
+// tanh(u) = u p(u^2): minimax polynomials, within 2e-8 (f32 rounding of their evaluation aside) for |u| up to 0.4 and
+// up to 1 (four and seven terms).
 constexpr float kTanhSmall = 0.4f, kTanhMid = 1.f;
 __host__ __device__ constexpr float tanh_small_coef(int i) {
   constexpr float c[4] = {0.999999573f, -0.333297261f, 0.132505672f, -0.0468257397f};

@@ -30,7 +30,7 @@
  *   skipped (its rows are not read) and RSWA_DEVICE_* bits are OR-ed into the
  *   status word of the workspace (or of `status` for rswa_append), which
  *   rswa_check_status reads back. No kernel traps.
- * - Outputs are f32. lse is the natural-log log-sum-exp of the scores a query
+ * - Outputs are f32 unless the call says otherwise. lse is the natural-log log-sum-exp of the scores a query
  *   attended to (-inf if it attended to nothing; out is then 0).
  * - Layout: per (sequence, head) every K/V row of head_dim 128 bf16 is 256
  *   contiguous bytes, and a sequence's rows for one head are contiguous, so a
@@ -105,8 +105,11 @@ RSWA_API int32_t rswa_version(void);
  * status word, per-(sequence, head) completion counters and split-KV
  * partials. It must be zero-filled once before its first use; every call that
  * completes leaves the counters at zero again, so it can be reused by later
- * calls on the same stream. Calls that share a workspace must not overlap in
- * time (use one workspace per stream). Returns 0 for invalid dims.
+ * calls of the same op with the same batch and heads on the same stream (of
+ * rswa_decode_scored and rswa_decode_shared: by later calls of either of any sizes
+ * that fit). Counters of one op lie where another's partials do: zero-fill the
+ * workspace in between, or give each op its own. Calls that share a workspace must
+ * not overlap in time (use one workspace per stream). Returns 0 for invalid dims.
  */
 RSWA_API size_t rswa_workspace_bytes(const rswa_dims* dims, int32_t op);
 

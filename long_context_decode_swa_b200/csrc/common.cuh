@@ -136,8 +136,10 @@ __device__ __forceinline__ void set_status(int32_t* status, int32_t bits) {
 // stream-serialisation attribute may start while the previous kernel in the
 // stream is still running. griddep_wait() blocks until that kernel has
 // completed and its writes are visible (it returns at once for a normal
-// launch), so every kernel here calls it before touching memory;
-// griddep_launch_dependents() lets the next kernel begin its prologue.
+// launch), so every kernel here calls it before touching memory, but for two launches that run
+// beside the one before them, which is the first part of their own call (balanced.cu's with a
+// shared part, scored_prefill.cu's late one): these call it before they read what that part
+// wrote, or end. griddep_launch_dependents() lets the next kernel begin its prologue.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

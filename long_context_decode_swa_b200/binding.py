@@ -217,6 +217,7 @@ def _tensors():
             native = _extension(_build.build_ext())
         except (RuntimeError, ImportError, OSError) as e:
             from . import tensors as native
+            _native = native
             warnings.warn(f"the tensor checks run in Python, 5 to 7 us a call more: {e}", RuntimeWarning, stacklevel=3)
         _native = native
     return _native
